@@ -63,6 +63,7 @@ extern "C" {
                                   |v| <= 65504: a step that meets a value beyond it (or a NaN) stores it
                                   saturated, leaves every sequence's state as it was, and fails with
                                   SPEC_ERR_RANGE */
+#define SPEC_DTYPE_F16 2       /* fp16 rows; only the spec_kv8_* calls take it */
 
 /* flags of spec_verify_tree_batch */
 #define SPEC_DEVICE_OUTPUTS 1  /* outputs are device pointers (or NULL); return without synchronising */
@@ -389,6 +390,153 @@ SPEC_API int spec_step_launches(spec_handle* h);
 SPEC_API int spec_lm_head_argmax_noalloc(const float* hidden, const void* final_norm, const void* lm_head, int M,
                                          int d, int V, float eps, int32_t* argmax, float* top1, float* top2,
                                          void* cuda_stream);
+
+/* ---- 8-bit paged K/V cache -------------------------------------------------
+ * A K/V cache in 8 bits, for callers that hold more or longer sequences than the
+ * handle's dense fp16 cache has room for (256 bytes per token and kv head
+ * instead of 768).  Three operators share it: spec_kv8_plan finds the pages and
+ * slots of new rows, spec_kv8_append stores rows, spec_kv8_attention attends over
+ * cached prefixes with the tree visibility of the verification step.
+ *
+ * Layout: pages of `page` tokens; codes[layer][K, V][page id][kv head][token][128]
+ * are e4m3, and exps[layer][K, V][page id][kv head] hold one exponent byte e per
+ * page and head: a stored value is code * 2^(e - 127).  The scale is a power of
+ * two so that a page whose later tokens need a larger one is rescaled by a shift
+ * of its codes' exponents: exact but for codes that become subnormal.  e - 127 is
+ * the least whole number of [-60, 120] with max |x| <= 448 * 2^(e - 127).
+ *
+ * Sequence s holds lengths[s] tokens; token i lies in page tables[s][i / page], at
+ * place i % page; its slot is that page id * page + the place.  lengths, tables
+ * and the ring of free pages are the caller's device buffers, so that no call
+ * below needs the host to know a length.
+ *
+ * The calls take device pointers of the GPU that was current at spec_kv8_open
+ * (it has to be current again at every call: SPEC_ERR_ARG otherwise), queue their
+ * work on cuda_stream (NULL: the legacy default stream), do not synchronise and
+ * allocate nothing; all can be captured into a CUDA graph.  Calls that touch the
+ * same pages or buffers have to be ordered by the caller. */
+typedef struct spec_kv8_config {
+  int32_t n_layers;
+  int32_t n_kv_heads;
+  int32_t head_dim;   /* 128 */
+  int32_t page;       /* tokens per page: 16, 32, 64 or 128 */
+  int32_t n_pages;    /* n_pages * page < 2^31 */
+} spec_kv8_config;
+
+typedef struct spec_kv8 spec_kv8;
+
+/* Bytes of the codes and of the exponents (0: configuration rejected). */
+SPEC_API size_t spec_kv8_code_bytes(const spec_kv8_config* cfg);
+SPEC_API size_t spec_kv8_exp_bytes(const spec_kv8_config* cfg);
+/* Record the borrowed buffers (codes 128-byte aligned; neither need be
+ * initialised: a page's exponent is set when its first token is stored). */
+SPEC_API int spec_kv8_open(const spec_kv8_config* cfg, void* codes, size_t code_bytes, void* exps, size_t exp_bytes,
+                           spec_kv8** out);
+/* Message of the last error on this handle ("" if none). */
+SPEC_API const char* spec_kv8_last_error(spec_kv8* h);
+/* Free host-side state; never the borrowed buffers. */
+SPEC_API void spec_kv8_close(spec_kv8* h);
+
+/* bits of the device status word that spec_kv8_plan writes (0: done) */
+#define SPEC_KV8_ROWS 1   /* more new rows than max_rows */
+#define SPEC_KV8_PAGES 2  /* more new pages than are free */
+#define SPEC_KV8_TABLE 4  /* a sequence outgrows max_blocks */
+#define SPEC_KV8_INDEX 8  /* a sequence id outside [0, n_seqs) or given twice, a length outside
+                             [0, max_blocks * page], or a state outside [0, n_pages) / [0, n_pages] */
+
+/* Lengths, pages and slots of a step.  Entry b of the batch (sequence s =
+ * seq_ids[b], or b) goes from lengths[s] to max(0, lengths[s] + add[b]) tokens:
+ * its new blocks get pages from the head of the ring of free pages, blocks that
+ * it no longer needs give theirs back at the tail (add = -2^30 ends a sequence).
+ * Pages given back are free for later calls, not for this one.  state = {head,
+ * count}: the free pages are ring[(head + i) % n_pages], i < count.
+ * Writes offsets (the first new row of every entry), slots (of the new rows, in
+ * entry order, then -1 up to max_rows), lengths_out (all n_seqs), state_out, status,
+ * the new blocks' entries of tables, and the ring's tail.  Nothing else of tables
+ * and ring changes, so the old lengths and state stay valid beside the new ones:
+ * a caller may keep both and drop either.  When status is not 0 nothing is done:
+ * tables and ring stay as they were, lengths_out and state_out repeat the input,
+ * offsets are 0 and slots -1. */
+typedef struct spec_kv8_plan_args {
+  const int32_t* lengths;  /* [n_seqs] */
+  const int32_t* add;      /* [batch] */
+  const int32_t* seq_ids;  /* [batch], distinct, or NULL: entry b is sequence b */
+  int32_t* tables;         /* [n_seqs][max_blocks] */
+  int32_t* ring;           /* [n_pages] */
+  const int32_t* state;    /* [2] */
+  int32_t* offsets;        /* [batch + 1] */
+  int32_t* slots;          /* [max_rows] */
+  int32_t* lengths_out;    /* [n_seqs]; may be lengths */
+  int32_t* state_out;      /* [2]; may be state */
+  int32_t* status;         /* [1] */
+  int32_t batch;           /* 1 .. 8192 */
+  int32_t n_seqs;          /* 1 .. 65536 */
+  int32_t max_blocks;
+  int32_t max_rows;        /* >= 0 */
+} spec_kv8_plan_args;
+SPEC_API int spec_kv8_plan(spec_kv8* h, const spec_kv8_plan_args* a, void* cuda_stream);
+
+/* Store K and V of `rows` rows into layer `layer`: row i is row src_rows[i] of k
+ * and v (or row i), and goes to slots[i].  A negative slot, or one outside the
+ * cache, or a source row outside [0, n_src), stores nothing.  Rows of one page
+ * have to follow each other with ascending slots, as spec_kv8_plan lists them; a
+ * page whose rows come in separate runs loses some of them.  The run that starts
+ * at place 0 opens its page (a new exponent); another one keeps the page's
+ * exponent or raises it, and then rescales the tokens before it.  Infinities are
+ * stored as the largest value of the page's scale, NaN as NaN. */
+typedef struct spec_kv8_append_args {
+  const void* k;           /* [n_src][n_kv_heads][128] with the strides below */
+  const void* v;
+  const int32_t* slots;    /* [rows] */
+  const int32_t* src_rows; /* [rows], or NULL */
+  int64_t k_row_stride, k_head_stride, v_row_stride, v_head_stride; /* in elements; rows of 16-byte alignment */
+  int32_t dtype;           /* SPEC_DTYPE_F32, _BF16 or _F16 */
+  int32_t rows;
+  int32_t n_src;
+} spec_kv8_append_args;
+SPEC_API int spec_kv8_append(spec_kv8* h, int layer, const spec_kv8_append_args* a, void* cuda_stream);
+
+/* Attention of the rows offsets[b] .. offsets[b + 1] - 1 of every entry b over
+ * layer `layer`.  A row sees the lengths[s] cached tokens of its sequence and, with
+ * k_new / v_new, those of its own step's rows that are its ancestors, itself
+ * included: parents[row] is the row's parent within its entry (-1, or a value
+ * outside [0, row within the entry): none); parents NULL: every earlier row.  Query
+ * head h reads kv head h / (n_q_heads / n_kv_heads).
+ *   out[row][h] = sum_j softmax_j(scale q.k_j) v_j,  lse[row][h] = ln sum_j exp(scale q.k_j)
+ * A row that sees nothing gets out 0 and lse -inf.  Rows beyond offsets[batch] are
+ * left as they were, as are those of an entry whose sequence id, length, row count
+ * (1 .. max_nodes) or offsets are out of range; a page id outside the cache reads
+ * as NaN.  out may not overlap the inputs.
+ * Infinities and NaN reach only the rows that see them. */
+typedef struct spec_kv8_attention_args {
+  const void* q;           /* [rows][n_q_heads][128] with the strides below */
+  const void* k_new;       /* [rows][n_kv_heads][128], or NULL: the cached prefix only */
+  const void* v_new;
+  const int32_t* parents;  /* [rows], or NULL */
+  const int32_t* offsets;  /* [batch + 1] */
+  const int32_t* tables;   /* [n_seqs][max_blocks] */
+  const int32_t* lengths;  /* [n_seqs] */
+  const int32_t* seq_ids;  /* [batch], or NULL: entry b is sequence b */
+  void* out;               /* [rows][n_q_heads][128], contiguous but for out_row_stride */
+  float* lse;              /* [rows][n_q_heads], or NULL */
+  void* workspace;         /* spec_kv8_attention_workspace() bytes, zero before its first use; calls that may
+                              overlap on the GPU need one each */
+  size_t workspace_bytes;
+  int64_t q_row_stride, q_head_stride, k_row_stride, k_head_stride, v_row_stride, v_head_stride,
+      out_row_stride;      /* in elements; rows of 16-byte alignment */
+  int32_t dtype;           /* of q, k_new, v_new and out: SPEC_DTYPE_BF16 or _F16 */
+  int32_t batch;
+  int32_t n_seqs;
+  int32_t max_blocks;
+  int32_t n_q_heads;       /* a multiple of n_kv_heads, at most 64 times it */
+  int32_t rows;            /* rows of q, k_new, v_new, parents and out */
+  int32_t max_nodes;       /* most rows of one entry: 1 .. 128 */
+  int32_t max_prefix;      /* no lengths[s] is above this (entries above it are left as they were) */
+  float scale;             /* > 0; 0: 1 / sqrt(128) */
+} spec_kv8_attention_args;
+/* Workspace bytes of spec_kv8_attention for these bounds. */
+SPEC_API size_t spec_kv8_attention_workspace(spec_kv8* h, int batch, int n_q_heads, int max_nodes, int max_prefix);
+SPEC_API int spec_kv8_attention(spec_kv8* h, int layer, const spec_kv8_attention_args* a, void* cuda_stream);
 
 /* Self-test of the bounded waits.  Every wait inside the library's kernels
  * (split-K and attention-chunk rendezvous, grid barriers between GEMM phases,

@@ -1,0 +1,34 @@
+// The 8-bit paged K/V cache: what its entry points and kernels share.  Not part
+// of the public C ABI.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "../../include/spec.h"
+
+namespace spec {
+
+constexpr int kKv8Hd = 128;      // head dimension
+constexpr int kKv8ExpMin = -60;  // exponents of the page scales (bias 127 in the byte)
+constexpr int kKv8ExpMax = 120;
+constexpr int kKv8MaxBatch = 8192;
+constexpr int kKv8MaxSeqs = 65536;
+constexpr int kKv8MaxGroup = 64;  // query heads per kv head
+constexpr int kKv8MaxNodes = 128;
+
+// One layer's planes of the cache.
+struct Kv8View {
+  uint8_t* codes[2];  // K, V: [page id][kv head][token][128]
+  uint8_t* exps[2];   // K, V: [page id][kv head]
+  int n_pages, page, page_log2, hkv;
+};
+
+cudaError_t kv8_plan_configure();
+cudaError_t launch_kv8_plan(const spec_kv8_plan_args& a, int page_log2, int n_pages, cudaStream_t s);
+cudaError_t launch_kv8_append(const Kv8View& c, const spec_kv8_append_args& a, int sm_count, cudaStream_t s);
+cudaError_t launch_kv8_attention(const Kv8View& c, const spec_kv8_attention_args& a, int sm_count, cudaStream_t s);
+
+}  // namespace spec

@@ -26,12 +26,19 @@ SPEC_ERR_RANGE = -9
 
 SPEC_DTYPE_F32 = 0
 SPEC_DTYPE_BF16 = 1
+SPEC_DTYPE_F16 = 2  # spec_kv8_* rows only
 
 SPEC_DEVICE_OUTPUTS = 1
 SPEC_DEBUG_LOGITS = 2
 SPEC_NO_GRAPH = 4
 SPEC_FEATURES = 8
 SPEC_DRAFT_TOPK = 10
+
+# status bits of spec_kv8_plan
+SPEC_KV8_ROWS = 1
+SPEC_KV8_PAGES = 2
+SPEC_KV8_TABLE = 4
+SPEC_KV8_INDEX = 8
 
 PROF_CLASSES = ("embed_meta", "gemm_qkv", "rope_kv_store", "attention", "gemm_o", "resid_norm", "gemm_gate_up",
                 "gemm_down", "lm_head", "lm_reduce", "accept_walk", "kv_compact", "gemm_layer", "draft_fc", "topk",
@@ -66,6 +73,35 @@ class spec_weights(ctypes.Structure):
         ("draft_layer", ctypes.POINTER(spec_layer_weights)), ("draft_final_norm", ctypes.c_void_p),
         ("draft_lm_head", ctypes.c_void_p), ("draft_vocab_ids", ctypes.c_void_p),
     ]
+
+
+class spec_kv8_config(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int32) for k in ("n_layers", "n_kv_heads", "head_dim", "page", "n_pages")]
+
+
+class spec_kv8_plan_args(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in
+                ("lengths", "add", "seq_ids", "tables", "ring", "state", "offsets", "slots", "lengths_out",
+                 "state_out", "status")] + \
+               [(k, ctypes.c_int32) for k in ("batch", "n_seqs", "max_blocks", "max_rows")]
+
+
+class spec_kv8_append_args(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("k", "v", "slots", "src_rows")] + \
+               [(k, ctypes.c_int64) for k in ("k_row_stride", "k_head_stride", "v_row_stride", "v_head_stride")] + \
+               [(k, ctypes.c_int32) for k in ("dtype", "rows", "n_src")]
+
+
+class spec_kv8_attention_args(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in
+                ("q", "k_new", "v_new", "parents", "offsets", "tables", "lengths", "seq_ids", "out", "lse",
+                 "workspace")] + \
+               [("workspace_bytes", ctypes.c_size_t)] + \
+               [(k, ctypes.c_int64) for k in ("q_row_stride", "q_head_stride", "k_row_stride", "k_head_stride",
+                                              "v_row_stride", "v_head_stride", "out_row_stride")] + \
+               [(k, ctypes.c_int32) for k in ("dtype", "batch", "n_seqs", "max_blocks", "n_q_heads", "rows",
+                                              "max_nodes", "max_prefix")] + \
+               [("scale", ctypes.c_float)]
 
 
 _i32p = ctypes.POINTER(ctypes.c_int32)
@@ -106,6 +142,17 @@ _SIGNATURES = {
     "spec_draft_append": (ctypes.c_int, [_h, ctypes.c_int, _vp, _i32p, ctypes.c_int]),
     "spec_draft_tree": (ctypes.c_int, [_h, ctypes.c_int, _i32p, _vp, _i32p, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                        _i32p, _i32p, _f32p]),
+    "spec_kv8_code_bytes": (ctypes.c_size_t, [ctypes.POINTER(spec_kv8_config)]),
+    "spec_kv8_exp_bytes": (ctypes.c_size_t, [ctypes.POINTER(spec_kv8_config)]),
+    "spec_kv8_open": (ctypes.c_int, [ctypes.POINTER(spec_kv8_config), _vp, ctypes.c_size_t, _vp, ctypes.c_size_t,
+                                     ctypes.POINTER(_h)]),
+    "spec_kv8_last_error": (ctypes.c_char_p, [_h]),
+    "spec_kv8_close": (None, [_h]),
+    # the argument structures: a pointer to one of the ctypes structures above, or its bytes
+    "spec_kv8_plan": (ctypes.c_int, [_h, _vp, _vp]),
+    "spec_kv8_append": (ctypes.c_int, [_h, ctypes.c_int, _vp, _vp]),
+    "spec_kv8_attention_workspace": (ctypes.c_size_t, [_h, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int]),
+    "spec_kv8_attention": (ctypes.c_int, [_h, ctypes.c_int, _vp, _vp]),
     "spec_wait_selftest": (ctypes.c_int, [_vp, ctypes.c_uint32, _i32p]),
     "spec_last_error": (ctypes.c_char_p, [_h]),
     "spec_free": (None, [_h]),
