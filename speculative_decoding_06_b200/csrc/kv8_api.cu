@@ -108,7 +108,7 @@ int spec_kv8_open(const spec_kv8_config* cfg, void* codes, size_t code_bytes, vo
     dev = -1;
     (void)cudaGetLastError();
   } else if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-             kv8_plan_configure() != cudaSuccess) {
+             kv8_plan_configure() != cudaSuccess || kv8_attention_configure() != cudaSuccess) {
     return SPEC_ERR_CUDA;
   }
   spec_kv8* h = new (std::nothrow) spec_kv8;
@@ -166,8 +166,10 @@ int spec_kv8_append(spec_kv8* h, int layer, const spec_kv8_append_args* a, void*
 }
 
 size_t spec_kv8_attention_workspace(spec_kv8* h, int batch, int n_q_heads, int max_nodes, int max_prefix) {
-  (void)h, (void)batch, (void)n_q_heads, (void)max_nodes, (void)max_prefix;
-  return 16;
+  if (!h || batch < 1 || n_q_heads < 1 || n_q_heads % h->cfg.n_kv_heads ||
+      n_q_heads / h->cfg.n_kv_heads > kKv8MaxGroup || max_nodes < 1 || max_nodes > kKv8MaxNodes || max_prefix < 0)
+    return 0;
+  return kv8_attention_workspace(view_of(h, 0), h->sm_count, batch, n_q_heads, max_nodes, max_prefix);
 }
 
 int spec_kv8_attention(spec_kv8* h, int layer, const spec_kv8_attention_args* a, void* cuda_stream) {

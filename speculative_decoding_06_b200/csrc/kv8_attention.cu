@@ -1,5 +1,31 @@
-// Attention over the 8-bit paged cache: the plain kernel, one warp per (row,
-// query head), a key at a time with the online softmax in 32 bits.
+// Attention over the 8-bit paged cache for few rows per kv head (plain decoding,
+// short chains and trees).
+//
+// Rows: the G = Hq / Hkv query heads of a kv head, for every row of an entry,
+// share that head's keys, so row r = node * G + g of a tile of 8 or 16 rows reads
+// each K/V byte once.  With few rows the work is bound by those bytes (256 per key
+// and head), not by arithmetic, so a warp keeps everything but the stream of
+// codes in registers:
+//
+//   scores   S^T = K Q^T by mma.m16n8k16: 16 keys by 8 rows.  The contraction's
+//            order is free, so lane (g, t) takes dimensions 16t.. and 64+16t.. of
+//            keys g and g + 8: whole 16-byte pieces, each word of codes (4 dims)
+//            one k-step's two A registers after e4m3 -> fp16 conversion (exact).
+//   softmax  in 32 bits, base 2, with a running maximum per row.  A page's K
+//            scale multiplies the scores; its V scale 2^w goes into the
+//            exponent: p' = 2^(x + w - m), m the running maximum of x + w, so
+//            that O sums p' times bare codes and l sums p' 2^-w.  p' is rounded to
+//            fp16 (2^-11 of itself) for the second product only.
+//   output   O^T = V^T P^T: lane (g, t) holds dimensions 16g .. 16g+15 of keys 2t,
+//            2t+1, 2t+8, 2t+9; two keys' bytes interleave into A registers;
+//            the scores' accumulators become the B operand by movmatrix.
+//
+// Each warp streams tiles of 32 keys through a private queue in shared memory
+// that it fills with cp.async (every thread reads only what it copied itself: no
+// barrier), three tiles deep.  The step's own rows (16-bit K and V) are added by
+// plain 32-bit arithmetic.  Warps, then the CTAs of a sequence cut into chunks,
+// merge their (m, l, O); of the latter the one that arrives last, in chunk order,
+// so that results do not depend on the order of arrival.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -10,80 +36,507 @@ namespace spec {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kTile = 32;          // keys per step of a warp: two groups of 16, each inside one page
+constexpr int kStages = 3;
+constexpr int kTileBytes = kTile * 2 * kKv8Hd;
+constexpr int kMaxChunk = 4096;    // keys of a CTA: its page ids and scales lie in shared memory
+constexpr int kGroups = kMaxChunk / 16;
 
-__device__ __forceinline__ float4 codes4(const uint8_t* p, float s) {
-  const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
-  const __nv_fp8_e4m3* h = reinterpret_cast<const __nv_fp8_e4m3*>(&w);
-  return make_float4((float)h[0] * s, (float)h[1] * s, (float)h[2] * s, (float)h[3] * s);
+struct DecodePlan {
+  int chunk, chunks, row_tiles;
+  float* part;   // [group][chunk][rows][128], then (m, l) [group][chunk][rows]
+  float2* ml;
+  int* counters; // [group]
+};
+
+struct Smem {
+  static constexpr int ring = 0;
+  static constexpr int page = ring + kWarps * kStages * kTileBytes;  // int [kGroups]: offset of a group's first row / 16
+  static constexpr int kscale = page + 4 * kGroups;                  // float [kGroups]: 2^e of K, NaN: no such page
+  static constexpr int vexp = kscale + 4 * kGroups;                  // float [kGroups]: e of V
+  static constexpr int anc = vexp + 4 * kGroups;                     // uint64 [16 rows][2]
+  static constexpr int misc = anc + 16 * 16;
+  static constexpr int end = misc + 16;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-template <typename T>
-__device__ __forceinline__ float4 rows4(const T* p) {
-  const uint2 w = *reinterpret_cast<const uint2*>(p);
-  const T* h = reinterpret_cast<const T*>(&w);
-  return make_float4(to_f32<T>(h[0]), to_f32<T>(h[1]), to_f32<T>(h[2]), to_f32<T>(h[3]));
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// two e4m3 codes (low byte first) as two fp16: exact
+__device__ __forceinline__ uint32_t cvt_e4m3x2(uint32_t w16) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(r) : "r"(w16));
+  return r;
+}
+__device__ __forceinline__ uint32_t cvt_e4m3x2_hi(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, b;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+__device__ __forceinline__ float finite_abs(float x) {
+  const float m = fabsf(x);
+  return m < INFINITY ? m : 0.f;
+}
+
+// Sixteen values of a 16-bit row as 32-bit floats.
 template <typename T>
-__global__ void __launch_bounds__(32 * kWarps) kv8_attention_plain_kernel(Kv8View c, spec_kv8_attention_args a) {
-  const int unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (unit >= a.rows * a.n_q_heads) return;
-  const int row = unit / a.n_q_heads, qh = unit - row * a.n_q_heads;
-  const int kvh = qh / (a.n_q_heads / c.hkv);
-  int b = -1;
-  for (int i = 0; i < a.batch; ++i)
-    if (a.offsets[i] <= row && row < a.offsets[i + 1]) b = i;
-  if (b < 0) return;
+__device__ __forceinline__ void load16(const T* p, float (&v)[16]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint4 r = __ldg(reinterpret_cast<const uint4*>(p) + h);
+    const T* e = reinterpret_cast<const T*>(&r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[8 * h + i] = to_f32<T>(e[i]);
+  }
+}
+
+template <typename T, int NT>
+__global__ void __launch_bounds__(kThreads) kv8_decode_kernel(Kv8View c, spec_kv8_attention_args a, DecodePlan pl) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  int* s_page = reinterpret_cast<int*>(smem + Smem::page);
+  float* s_kscale = reinterpret_cast<float*>(smem + Smem::kscale);
+  float* s_vexp = reinterpret_cast<float*>(smem + Smem::vexp);
+  uint64_t* s_anc = reinterpret_cast<uint64_t*>(smem + Smem::anc);
+  int* s_last = reinterpret_cast<int*>(smem + Smem::misc);
+  constexpr int kRows = 8 * NT;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int G = a.n_q_heads / c.hkv;
+  const int group = blockIdx.x / pl.chunks, chunk_i = blockIdx.x - group * pl.chunks;
+  const int bk = group / pl.row_tiles, row0 = (group - bk * pl.row_tiles) * kRows;
+  const int b = bk / c.hkv, kvh = bk - b * c.hkv;
   const int first = a.offsets[b], n = a.offsets[b + 1] - first;
   const int seq = a.seq_ids ? a.seq_ids[b] : b;
-  if (first < 0 || n > a.max_nodes || first + n > a.rows || seq < 0 || seq >= a.n_seqs) return;
+  if (seq < 0 || seq >= a.n_seqs || first < 0 || n < 1 || n > a.max_nodes || n > a.rows - first) return;
   const int P = a.lengths[seq];
-  if (P < 0 || P > a.max_prefix) return;
-  const float4 q = rows4(reinterpret_cast<const T*>(a.q) + a.q_row_stride * row + a.q_head_stride * qh + 4 * lane);
-  float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto see = [&](float4 k, float4 v) {
-    const float s = warp_sum(q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w) * a.scale;
-    const float m2 = fmaxf(m, s);
-    const float keep = m2 == m ? 1.f : expf(m - m2), p = expf(s - m2);
-    m = m2;
-    l = l * keep + p;
-    o = make_float4(o.x * keep + p * v.x, o.y * keep + p * v.y, o.z * keep + p * v.z, o.w * keep + p * v.w);
-  };
-  for (int j = 0; j < P; ++j) {
-    const int pg = a.tables[(size_t)seq * a.max_blocks + (j >> c.page_log2)];
-    if (pg < 0 || pg >= c.n_pages) {
-      see(make_float4(NAN, NAN, NAN, NAN), make_float4(NAN, NAN, NAN, NAN));
-      continue;
+  const int rows = n * G;
+  if (P < 0 || P > a.max_prefix || row0 >= rows) return;
+  const int nc = max(1, (P + pl.chunk - 1) / pl.chunk);
+  if (chunk_i >= nc) return;
+  const int c0 = chunk_i * pl.chunk, c1 = min(P, c0 + pl.chunk);
+  const int ngroups = (c1 - c0 + 15) >> 4;
+  const int ntiles = (c1 - c0 + kTile - 1) / kTile;
+
+  // pages of the chunk's groups of 16 keys
+  for (int i = tid; i < 2 * ntiles; i += kThreads) {
+    const int key = c0 + 16 * i;
+    int pg = 0;
+    float ks = 0.f, ve = 0.f;
+    if (i < ngroups) {
+      pg = a.tables[(size_t)seq * a.max_blocks + (key >> c.page_log2)];
+      const bool ok = pg >= 0 && pg < c.n_pages;
+      if (!ok) pg = 0;
+      const size_t at = (size_t)pg * c.hkv + kvh;
+      ks = ok ? __int_as_float((int)c.exps[0][at] << 23) : NAN;
+      ve = (float)((int)c.exps[1][at] - 127);
     }
-    const size_t ph = (size_t)pg * c.hkv + kvh;
-    const size_t at = ((ph << c.page_log2) + (j & (c.page - 1))) * kKv8Hd + 4 * lane;
-    see(codes4(c.codes[0] + at, exp2f((float)c.exps[0][ph] - 127.f)),
-        codes4(c.codes[1] + at, exp2f((float)c.exps[1][ph] - 127.f)));
+    s_page[i] = (((pg * c.hkv + kvh) << c.page_log2) + (key & (c.page - 1))) >> 4;
+    s_kscale[i] = ks;
+    s_vexp[i] = ve;
   }
-  for (int j = row - first; a.k_new && j >= 0;) {
-    see(rows4(reinterpret_cast<const T*>(a.k_new) + a.k_row_stride * (first + j) + a.k_head_stride * kvh + 4 * lane),
-        rows4(reinterpret_cast<const T*>(a.v_new) + a.v_row_stride * (first + j) + a.v_head_stride * kvh + 4 * lane));
-    const int up = a.parents ? a.parents[first + j] : j - 1;
-    j = up < j ? up : -1;
+  // ancestors of the tile's rows among the step's rows (itself included)
+  if (a.k_new && tid < kRows) {
+    uint64_t lo = 0, hi = 0;
+    if (row0 + tid < rows) {
+      int j = (row0 + tid) / G;
+      if (!a.parents) {
+        lo = j >= 63 ? ~0ull : (2ull << j) - 1;
+        hi = j < 64 ? 0 : j >= 127 ? ~0ull : (2ull << (j - 64)) - 1;
+      } else {
+        while (j >= 0) {
+          if (j < 64) lo |= 1ull << j;
+          else hi |= 1ull << (j - 64);
+          const int up = a.parents[first + j];
+          j = up < j ? up : -1;
+        }
+      }
+    }
+    s_anc[2 * tid] = lo;
+    s_anc[2 * tid + 1] = hi;
   }
-  const bool any = l > 0.f || isnan(l);
-  const float inv = any ? 1.f / l : 0.f;
-  T* out = reinterpret_cast<T*>(a.out) + a.out_row_stride * row + qh * kKv8Hd + 4 * lane;
-  out[0] = from_f32<T>(o.x * inv);
-  out[1] = from_f32<T>(o.y * inv);
-  out[2] = from_f32<T>(o.z * inv);
-  out[3] = from_f32<T>(o.w * inv);
-  if (a.lse && lane == 0) a.lse[(size_t)row * a.n_q_heads + qh] = any ? m + logf(l) : -INFINITY;
+  // this lane's part of q, as fp16 pieces of row g (+ 8): bf16 rows are scaled by a
+  // power of two that puts their largest value near 2^8 (fp16 then holds every value
+  // down to 2^-32 of it)
+  uint32_t qf[NT][16];
+  float qs[NT];  // row g's factor, with scale * log2(e)
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = row0 + 8 * nt + g;
+    const int rr = min(r, rows - 1);
+    const int node = rr / G;
+    const T* p = reinterpret_cast<const T*>(a.q) + a.q_row_stride * (first + node) +
+                 a.q_head_stride * (kvh * G + (rr - node * G)) + 16 * t;
+    float v[32];
+    load16(p, reinterpret_cast<float(&)[16]>(v[0]));
+    load16(p + 64, reinterpret_cast<float(&)[16]>(v[16]));
+    int ex = 0;
+    if (sizeof(T) == 2 && !__is_same(T, __half)) {
+      float m = 0.f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) m = fmaxf(m, finite_abs(v[i]));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      ex = max(-100, min(100, (__float_as_int(m) >> 23) - 127 - 8));
+    }
+    const float f = __int_as_float((127 - ex) << 23);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const __half2 h = __floats2half2_rn(v[2 * i] * f, v[2 * i + 1] * f);
+      qf[nt][i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    qs[nt] = a.scale * 1.4426950408889634f * __int_as_float((127 + ex) << 23);
+  }
+  // the factors of this lane's accumulator columns, rows 2t and 2t + 1
+  float qc[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    qc[nt][0] = __shfl_sync(0xffffffffu, qs[nt], 8 * t);
+    qc[nt][1] = __shfl_sync(0xffffffffu, qs[nt], 8 * t + 4);
+  }
+  __syncthreads();
+
+  const uint32_t ring = smem_u32(smem + Smem::ring) + warp * (kStages * kTileBytes) + lane * 16;
+  const int mine = ntiles > warp ? (ntiles - warp + kWarps - 1) / kWarps : 0;
+  auto fetch = [&](int i) {
+    if (i < mine) {
+      const uint32_t dst = ring + (i % kStages) * kTileBytes;
+      const int g0 = 2 * (warp + kWarps * i);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const size_t base = (size_t)s_page[g0 + u] * (16 * kKv8Hd);
+        const uint8_t* k = c.codes[0] + base + g * kKv8Hd + 16 * t;
+        const uint8_t* v = c.codes[1] + base + 2 * t * kKv8Hd + 16 * g;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          cp_async16(dst + (8 * u + j) * 512, k + (j >> 1) * 8 * kKv8Hd + (j & 1) * 64);
+          cp_async16(dst + (8 * u + 4 + j) * 512, v + ((j >> 1) * 8 + (j & 1)) * kKv8Hd);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(i);
+
+  float m[NT][2], l[NT][2], o[NT][8][4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    m[nt][0] = m[nt][1] = -INFINITY;
+    l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) o[nt][i][q] = 0.f;
+  }
+  // a row's running maximum rises to m2: what was summed shrinks
+  auto raise = [&](int nt, int col, float m2) {
+    const float keep = m2 > m[nt][col] ? fast_exp2(m[nt][col] - m2) : 1.f;
+    m[nt][col] = fmaxf(m[nt][col], m2);
+    l[nt][col] *= keep;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      o[nt][i][col] *= keep;
+      o[nt][i][2 + col] *= keep;
+    }
+  };
+
+  for (int i = 0; i < mine; ++i) {
+    fetch(i + kStages - 1);
+    cp_async_wait<kStages - 1>();
+    const uint4* buf = reinterpret_cast<const uint4*>(smem + Smem::ring + warp * (kStages * kTileBytes) +
+                                                      (i % kStages) * kTileBytes) + lane;
+    const int g0 = 2 * (warp + kWarps * i);
+    float s[2][NT][4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint4 ka0 = buf[(8 * u + 0) * 32], ka1 = buf[(8 * u + 1) * 32];  // key g
+      const uint4 kb0 = buf[(8 * u + 2) * 32], kb1 = buf[(8 * u + 3) * 32];  // key g + 8
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) s[u][nt][0] = s[u][nt][1] = s[u][nt][2] = s[u][nt][3] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        const uint32_t wa = word(ks < 4 ? ka0 : ka1, ks & 3), wb = word(ks < 4 ? kb0 : kb1, ks & 3);
+        const uint32_t a0 = cvt_e4m3x2(wa), a2 = cvt_e4m3x2_hi(wa), a1 = cvt_e4m3x2(wb), a3 = cvt_e4m3x2_hi(wb);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma16816(s[u][nt], a0, a1, a2, a3, qf[nt][2 * ks], qf[nt][2 * ks + 1]);
+      }
+    }
+    // x + w in base 2, hidden keys at -inf
+    const float ks0 = s_kscale[g0], ks1 = s_kscale[g0 + 1], ve0 = s_vexp[g0], ve1 = s_vexp[g0 + 1];
+    const int left = c1 - (c0 + 16 * g0);  // keys of the tile that exist
+    uint32_t pb[2][NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float ks = u ? ks1 : ks0, ve = u ? ve1 : ve0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float x = fmaf(s[u][nt][q], qc[nt][q & 1] * ks, ve);
+          s[u][nt][q] = 16 * u + g + (q >> 1) * 8 < left ? x : -INFINITY;
+        }
+      }
+      bool up = false;
+      float mx[2];
+#pragma unroll
+      for (int col = 0; col < 2; ++col) {
+        float v = fmaxf(fmaxf(s[0][nt][col], s[0][nt][2 + col]), fmaxf(s[1][nt][col], s[1][nt][2 + col]));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+        mx[col] = v;
+        up |= v > m[nt][col];
+      }
+      if (__any_sync(0xffffffffu, up)) {
+        raise(nt, 0, mx[0]);
+        raise(nt, 1, mx[1]);
+      }
+      const float n0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], n1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float un = fast_exp2(-(u ? ve1 : ve0));
+        const float p0 = fast_exp2(s[u][nt][0] - n0), p1 = fast_exp2(s[u][nt][1] - n1);
+        const float p2 = fast_exp2(s[u][nt][2] - n0), p3 = fast_exp2(s[u][nt][3] - n1);
+        l[nt][0] = fmaf(p0 + p2, un, l[nt][0]);
+        l[nt][1] = fmaf(p1 + p3, un, l[nt][1]);
+        const __half2 lo = __floats2half2_rn(p0, p1), hi = __floats2half2_rn(p2, p3);
+        pb[u][nt][0] = transpose8x8(*reinterpret_cast<const uint32_t*>(&lo));
+        pb[u][nt][1] = transpose8x8(*reinterpret_cast<const uint32_t*>(&hi));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      uint4 v0 = buf[(8 * u + 4) * 32], v1 = buf[(8 * u + 5) * 32], v2 = buf[(8 * u + 6) * 32], v3 = buf[(8 * u + 7) * 32];
+      if (left < 16 * u + 16) {  // what lies behind the sequence's end may be anything: 0 * NaN would spread
+        const int k0 = left - 16 * u - 2 * t;
+        if (k0 <= 0) v0 = make_uint4(0, 0, 0, 0);
+        if (k0 <= 1) v1 = make_uint4(0, 0, 0, 0);
+        if (k0 <= 8) v2 = make_uint4(0, 0, 0, 0);
+        if (k0 <= 9) v3 = make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t x0 = word(v0, w), x1 = word(v1, w), x2 = word(v2, w), x3 = word(v3, w);
+        const uint32_t e0 = __byte_perm(x0, x1, 0x5140), e1 = __byte_perm(x0, x1, 0x7362);
+        const uint32_t f0 = __byte_perm(x2, x3, 0x5140), f1 = __byte_perm(x2, x3, 0x7362);
+        const uint32_t a0 = cvt_e4m3x2(e0), a1 = cvt_e4m3x2_hi(e0), a2 = cvt_e4m3x2(f0), a3 = cvt_e4m3x2_hi(f0);
+        const uint32_t b0 = cvt_e4m3x2(e1), b1 = cvt_e4m3x2_hi(e1), b2 = cvt_e4m3x2(f1), b3 = cvt_e4m3x2_hi(f1);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma16816(o[nt][2 * w], a0, a1, a2, a3, pb[u][nt][0], pb[u][nt][1]);
+          mma16816(o[nt][2 * w + 1], b0, b1, b2, b3, pb[u][nt][0], pb[u][nt][1]);
+        }
+      }
+    }
+  }
+  cp_async_wait<0>();
+
+  // the step's own rows: the last chunk's CTA, its warps in turn
+  if (a.k_new && chunk_i == nc - 1) {
+    // rows of the tile see no row behind the tile's last node
+    const int top = min(n - 1, (row0 + kRows - 1) / G);
+    for (int j = warp; j <= top; j += kWarps) {
+      const T* kp = reinterpret_cast<const T*>(a.k_new) + a.k_row_stride * (first + j) + a.k_head_stride * kvh + 16 * t;
+      const T* vp = reinterpret_cast<const T*>(a.v_new) + a.v_row_stride * (first + j) + a.v_head_stride * kvh + 16 * g;
+      float k[32], v[16];
+      load16(kp, reinterpret_cast<float(&)[16]>(k[0]));
+      load16(kp + 64, reinterpret_cast<float(&)[16]>(k[16]));
+      load16(vp, v);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float x = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&qf[nt][i]));
+          x = fmaf(q.x, k[2 * i], x);
+          x = fmaf(q.y, k[2 * i + 1], x);
+        }
+        x += __shfl_xor_sync(0xffffffffu, x, 1);
+        x += __shfl_xor_sync(0xffffffffu, x, 2);
+        x *= qs[nt];
+        const bool sees = (s_anc[2 * (8 * nt + g) + (j >> 6)] >> (j & 63)) & 1;
+        x = sees ? x : -INFINITY;
+#pragma unroll
+        for (int col = 0; col < 2; ++col) {
+          const float xc = __shfl_sync(0xffffffffu, x, 8 * t + 4 * col);
+          const bool see = __shfl_sync(0xffffffffu, (int)sees, 8 * t + 4 * col);
+          if (!see) continue;
+          raise(nt, col, xc);
+          const float p = fast_exp2(xc - (m[nt][col] == -INFINITY ? 0.f : m[nt][col]));
+          if (g == 0) l[nt][col] += p;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            o[nt][i][col] = fmaf(p, v[2 * i], o[nt][i][col]);
+            o[nt][i][2 + col] = fmaf(p, v[2 * i + 1], o[nt][i][2 + col]);
+          }
+        }
+      }
+    }
+  }
+
+  // merge the warps: (m, l) and O of each into shared memory (the queues are empty)
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int col = 0; col < 2; ++col) {
+      l[nt][col] += __shfl_xor_sync(0xffffffffu, l[nt][col], 4);
+      l[nt][col] += __shfl_xor_sync(0xffffffffu, l[nt][col], 8);
+      l[nt][col] += __shfl_xor_sync(0xffffffffu, l[nt][col], 16);
+    }
+  __syncthreads();
+  float* s_o = reinterpret_cast<float*>(smem + Smem::ring);             // [warp][rows][132]
+  float2* s_ml = reinterpret_cast<float2*>(s_o + kWarps * kRows * 132);  // [warp][rows]
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int col = 0; col < 2; ++col) {
+      const int r = warp * kRows + 8 * nt + 2 * t + col;
+      if (g == 0) s_ml[r] = make_float2(m[nt][col], l[nt][col]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<float2*>(&s_o[r * 132 + 16 * g + 2 * i]) = make_float2(o[nt][i][col], o[nt][i][2 + col]);
+    }
+  __syncthreads();
+  // a warp per row, a lane per four dimensions
+  auto finish = [&](int r, float mm, float ll, float4 acc) {
+    const int node = r / G, head = kvh * G + (r - node * G);
+    const float inv = ll == 0.f ? 0.f : 1.f / ll;
+    T* out = reinterpret_cast<T*>(a.out) + a.out_row_stride * (first + node) + (size_t)head * kKv8Hd + 4 * lane;
+    T w[4] = {from_f32<T>(acc.x * inv), from_f32<T>(acc.y * inv), from_f32<T>(acc.z * inv), from_f32<T>(acc.w * inv)};
+    *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(w);
+    if (a.lse && lane == 0)
+      a.lse[(size_t)(first + node) * a.n_q_heads + head] =
+          ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f;
+  };
+  const size_t slot = (size_t)group * pl.chunks + chunk_i;
+  for (int r = warp; r < kRows && row0 + r < rows; r += kWarps) {
+    float mm = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_ml[w * kRows + r].x);
+    float ll = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float2 x = s_ml[w * kRows + r];
+      const float f = x.x == -INFINITY && x.y == 0.f ? 0.f : fast_exp2(x.x - mm);
+      const float4 v = *reinterpret_cast<const float4*>(&s_o[(w * kRows + r) * 132 + 4 * lane]);
+      ll = fmaf(f, x.y, ll);
+      acc = make_float4(fmaf(f, v.x, acc.x), fmaf(f, v.y, acc.y), fmaf(f, v.z, acc.z), fmaf(f, v.w, acc.w));
+    }
+    if (nc == 1) {
+      finish(row0 + r, mm, ll, acc);
+    } else {
+      __stcg(reinterpret_cast<float4*>(pl.part + (slot * kRows + r) * kKv8Hd) + lane, acc);
+      if (lane == 0) __stcg(&pl.ml[slot * kRows + r], make_float2(mm, ll));
+    }
+  }
+  if (nc == 1) return;
+  // the sequence's last CTA to arrive merges the chunks and leaves the counter at zero
+  __threadfence();
+  __syncthreads();
+  if (tid == 0) *s_last = atomicAdd(&pl.counters[group], 1) == nc - 1;
+  __syncthreads();
+  if (!*s_last) return;
+  __threadfence();
+  if (tid == 0) pl.counters[group] = 0;
+  const size_t slot0 = (size_t)group * pl.chunks;
+  for (int r = warp; r < kRows && row0 + r < rows; r += kWarps) {
+    float mm = -INFINITY;
+    for (int k = lane; k < nc; k += 32) mm = fmaxf(mm, __ldcg(&pl.ml[(slot0 + k) * kRows + r]).x);
+    mm = warp_max(mm);
+    float ll = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < nc; ++k) {
+      const float2 x = __ldcg(&pl.ml[(slot0 + k) * kRows + r]);
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(pl.part + ((slot0 + k) * kRows + r) * kKv8Hd) + lane);
+      const float f = x.x == -INFINITY && x.y == 0.f ? 0.f : fast_exp2(x.x - mm);
+      ll = fmaf(f, x.y, ll);
+      acc = make_float4(fmaf(f, v.x, acc.x), fmaf(f, v.y, acc.y), fmaf(f, v.z, acc.z), fmaf(f, v.w, acc.w));
+    }
+    finish(row0 + r, mm, ll, acc);
+  }
+}
+
+// Rows per tile, chunks and workspace for the given bounds.
+DecodePlan plan_decode(int hkv, int sm_count, int batch, int n_q_heads, int max_nodes, int max_prefix, int* nt,
+                       size_t* bytes) {
+  DecodePlan p{};
+  const int rows = max_nodes * (n_q_heads / hkv);
+  *nt = rows <= 8 ? 1 : 2;
+  p.row_tiles = (rows + 8 * *nt - 1) / (8 * *nt);
+  const long long groups = (long long)batch * hkv * p.row_tiles;
+  // about four rounds of two CTAs per SM, at least a tile for each warp
+  const long long want = groups * max_prefix / (8LL * sm_count);
+  long long chunk = (want + 127) / 128 * 128;
+  chunk = chunk < 128 ? 128 : chunk > kMaxChunk ? kMaxChunk : chunk;
+  p.chunk = (int)chunk;
+  p.chunks = (int)((max_prefix + chunk - 1) / chunk);
+  if (p.chunks < 1) p.chunks = 1;
+  size_t n = 16;
+  if (p.chunks > 1) {
+    const size_t slots = (size_t)groups * p.chunks * 8 * *nt;
+    n = (4 * (size_t)groups + 255) / 256 * 256 + slots * (kKv8Hd * 4 + 8);
+  }
+  *bytes = n;
+  return p;
 }
 
 }  // namespace
 
+size_t kv8_attention_workspace(const Kv8View& c, int sm_count, int batch, int n_q_heads, int max_nodes, int max_prefix) {
+  int nt = 1;
+  size_t bytes = 0;
+  plan_decode(c.hkv, sm_count, batch, n_q_heads, max_nodes, max_prefix, &nt, &bytes);
+  return bytes;
+}
+
+cudaError_t kv8_attention_configure() {
+  cudaError_t e = cudaSuccess;
+  for (const void* f : {(const void*)kv8_decode_kernel<__nv_bfloat16, 1>, (const void*)kv8_decode_kernel<__nv_bfloat16, 2>,
+                        (const void*)kv8_decode_kernel<__half, 1>, (const void*)kv8_decode_kernel<__half, 2>})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::end);
+  return e;
+}
+
 cudaError_t launch_kv8_attention(const Kv8View& c, const spec_kv8_attention_args& a, int sm_count, cudaStream_t s) {
-  (void)sm_count;
-  const int grid = (a.rows * a.n_q_heads + kWarps - 1) / kWarps;
-  if (a.dtype == SPEC_DTYPE_BF16) kv8_attention_plain_kernel<__nv_bfloat16><<<grid, 32 * kWarps, 0, s>>>(c, a);
-  else kv8_attention_plain_kernel<__half><<<grid, 32 * kWarps, 0, s>>>(c, a);
+  int nt = 1;
+  size_t bytes = 0;
+  DecodePlan p = plan_decode(c.hkv, sm_count, a.batch, a.n_q_heads, a.max_nodes, a.max_prefix, &nt, &bytes);
+  const size_t groups = (size_t)a.batch * c.hkv * p.row_tiles;
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  p.counters = reinterpret_cast<int*>(ws);
+  p.ml = reinterpret_cast<float2*>(ws + (4 * groups + 255) / 256 * 256);
+  p.part = reinterpret_cast<float*>(p.ml + groups * p.chunks * 8 * nt);
+  const unsigned grid = (unsigned)(groups * p.chunks);
+  if (a.dtype == SPEC_DTYPE_BF16) {
+    if (nt == 1) kv8_decode_kernel<__nv_bfloat16, 1><<<grid, kThreads, Smem::end, s>>>(c, a, p);
+    else kv8_decode_kernel<__nv_bfloat16, 2><<<grid, kThreads, Smem::end, s>>>(c, a, p);
+  } else {
+    if (nt == 1) kv8_decode_kernel<__half, 1><<<grid, kThreads, Smem::end, s>>>(c, a, p);
+    else kv8_decode_kernel<__half, 2><<<grid, kThreads, Smem::end, s>>>(c, a, p);
+  }
   return cudaGetLastError();
 }
 
