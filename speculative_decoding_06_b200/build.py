@@ -1,4 +1,5 @@
-"""Build libspec.so (the C-ABI library) in-tree with nvcc for sm_100a.
+"""Build libspec.so (the C-ABI library) in-tree with nvcc for sm_100a, and _kv8 (the torch binding of its 8-bit
+cache) with the host compiler.
 
     python -m speculative_decoding_06_b200.build [--force] [-v]
 
@@ -14,12 +15,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libspec.so")
+BINDING = os.path.join(PKG, "_kv8" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -76,7 +79,32 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             sys.stderr.write(" ".join(cmd) + "\n" + res.stdout + res.stderr)
         if res.returncode:
             raise RuntimeError("link failed")
+    build_binding(force, verbose)
     return LIB
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """The torch binding: includes torch's headers, linked with libspec.so beside it."""
+    src = os.path.join(CSRC, "kv8_torch.cpp")
+    if not force and not _stale(BINDING, [src, os.path.join(ROOT, "include", "spec.h")]):
+        return BINDING
+    import torch
+    tdir = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch.compiled_with_cxx11_abi()]
+    for d in (os.path.join(tdir, "include"), os.path.join(tdir, "include", "torch", "csrc", "api", "include"),
+              os.path.join(cuda, "include"), sysconfig.get_paths()["include"], os.path.join(ROOT, "include")):
+        cmd += ["-isystem", d]
+    cmd += [src, "-o", BINDING, "-L" + PKG, "-l:libspec.so", "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(tdir, "lib"),
+            "-Wl,-rpath," + os.path.join(tdir, "lib"), "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu",
+            "-ltorch_python"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if verbose or res.returncode:
+        sys.stderr.write(" ".join(cmd) + "\n" + res.stdout + res.stderr)
+    if res.returncode:
+        raise RuntimeError("g++ failed on %s" % src)
+    return BINDING
 
 
 if __name__ == "__main__":
