@@ -402,7 +402,8 @@ SPEC_API int spec_lm_head_argmax_noalloc(const float* hidden, const void* final_
  * are e4m3, and exps[layer][K, V][page id][kv head] hold one exponent byte e per
  * page and head: a stored value is code * 2^(e - 127).  The scale is a power of
  * two so that a page whose later tokens need a larger one is rescaled by a shift
- * of its codes' exponents: exact but for codes that become subnormal.  e - 127 is
+ * of its codes' exponents: exact but for codes that become subnormal.  e = 255
+ * stands for NaN; the codes 0x7F and 0xFF do not occur in pages without it.  e - 127 is
  * the least whole number of [-60, 120] with max |x| <= 448 * 2^(e - 127).
  *
  * Sequence s holds lengths[s] tokens; token i lies in page tables[s][i / page], at
@@ -483,7 +484,9 @@ SPEC_API int spec_kv8_plan(spec_kv8* h, const spec_kv8_plan_args* a, void* cuda_
  * page whose rows come in separate runs loses some of them.  The run that starts
  * at place 0 opens its page (a new exponent); another one keeps the page's
  * exponent or raises it, and then rescales the tokens before it.  Infinities are
- * stored as the largest value of the page's scale, NaN as NaN. */
+ * stored as the largest value of the page's scale.  A NaN sets the exponent of its
+ * page and head to 255: all of that page and head reads as NaN until it is opened
+ * anew (its codes are then unspecified). */
 typedef struct spec_kv8_append_args {
   const void* k;           /* [n_src][n_kv_heads][128] with the strides below */
   const void* v;
@@ -506,8 +509,9 @@ SPEC_API int spec_kv8_append(spec_kv8* h, int layer, const spec_kv8_append_args*
  * A row that sees nothing gets out 0 and lse -inf.  Rows beyond offsets[batch] are
  * left as they were, as are those of an entry whose sequence id, length, row count
  * (1 .. max_nodes) or offsets are out of range; a page id outside the cache reads
- * as NaN.  out may not overlap the inputs.
- * Infinities and NaN reach only the rows that see them. */
+ * as NaN.  out may not overlap the inputs.  Infinities and NaN in q, k_new and v_new
+ * reach only the rows that see them, whatever lies in the cache behind a sequence's
+ * end none. */
 typedef struct spec_kv8_attention_args {
   const void* q;           /* [rows][n_q_heads][128] with the strides below */
   const void* k_new;       /* [rows][n_kv_heads][128], or NULL: the cached prefix only */

@@ -56,6 +56,9 @@ def append(codes, exps, page, k, v, slots, src_rows=None):
         for plane, x in ((0, k), (1, v)):
             for h in range(codes.shape[2]):
                 new = np.stack([np.asarray(x[r][h], np.float64) for _, r in rows[i:j]])
+                if np.isnan(new).any() or (place and exps[plane, pg, h] == 255):
+                    exps[plane, pg, h] = 255  # NaN: the codes are unspecified
+                    continue
                 e = exponent(np.max(np.abs(new), where=np.isfinite(new), initial=0.0))
                 if place:
                     old = int(exps[plane, pg, h]) - BIAS
@@ -140,7 +143,8 @@ def attention(codes, exps, page, q, tables, lengths, offsets, scale, k_new=None,
             for j in range(P):
                 pg = int(tables[s, j // page])
                 if 0 <= pg < n_pages:
-                    x[j] = E4M3[codes[plane, pg, :, j % page]] * 2.0 ** (exps[plane, pg].astype(np.float64) - BIAS)[:, None]
+                    e = np.where(exps[plane, pg] == 255, np.nan, exps[plane, pg].astype(np.float64) - BIAS)
+                    x[j] = E4M3[codes[plane, pg, :, j % page]] * (2.0 ** e)[:, None]
             cached.append(x)
         for i in range(hi - lo):
             seen, j = [], i

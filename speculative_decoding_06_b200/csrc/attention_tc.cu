@@ -107,19 +107,6 @@ constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kKeys >> 3) << 17) | ((uint
 constexpr uint32_t kIdescS2 = (1u << 4) | ((uint32_t)(2 * kKeys >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
 constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | ((uint32_t)(128 >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
 
-// MN-major operand with the 128-byte swizzle: 64 fp16 along N per 128-byte row,
-// 8-row (K) groups 1024 B apart (stride byte offset), N atoms `lbo` bytes apart
-// (leading byte offset).
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr, uint32_t lbo) {
-  uint64_t d = 0;
-  d |= (uint64_t)((smem_addr & 0x3FFFF) >> 4);
-  d |= (uint64_t)((lbo >> 4) & 0x3FFF) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
-
 // optional timeline: trace[cta][k] = %globaltimer at mark k (thread 0 of the
 // softmax warps, or the issuing thread for marks 1, 2, 11, 12)
 constexpr int kTraceMarks = 16;

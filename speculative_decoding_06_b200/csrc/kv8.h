@@ -18,6 +18,8 @@ constexpr int kKv8MaxBatch = 8192;
 constexpr int kKv8MaxSeqs = 65536;
 constexpr int kKv8MaxGroup = 64;  // query heads per kv head
 constexpr int kKv8MaxNodes = 128;
+constexpr int kKv8TcMaxChunks = 8;     // CTAs of a cluster that share a sequence's prefix (tree kernel)
+constexpr int kKv8TcMaxKeys = 49152;   // keys of one of them
 
 // One layer's planes of the cache.
 struct Kv8View {
@@ -32,5 +34,9 @@ cudaError_t launch_kv8_append(const Kv8View& c, const spec_kv8_append_args& a, i
 cudaError_t kv8_attention_configure();
 size_t kv8_attention_workspace(const Kv8View& c, int sm_count, int batch, int n_q_heads, int max_nodes, int max_prefix);
 cudaError_t launch_kv8_attention(const Kv8View& c, const spec_kv8_attention_args& a, int sm_count, cudaStream_t s);
+
+// rows > 16 per kv head: the tensor-core kernel (prefixes up to kKv8TcMaxChunks * kKv8TcMaxKeys; no workspace)
+cudaError_t kv8_tree_configure();
+cudaError_t launch_kv8_tree(const Kv8View& c, const spec_kv8_attention_args& a, int sm_count, cudaStream_t s);
 
 }  // namespace spec

@@ -34,7 +34,7 @@ int fail(spec_kv8* h, int code, const char* fmt, ...) {
 }
 
 bool config_ok(const spec_kv8_config* c) {
-  return c && c->n_layers >= 1 && c->n_kv_heads >= 1 && c->head_dim == kKv8Hd &&
+  return c && c->n_layers >= 1 && c->n_kv_heads >= 1 && c->n_kv_heads <= 65535 && c->head_dim == kKv8Hd &&
          (c->page == 16 || c->page == 32 || c->page == 64 || c->page == 128) && c->n_pages >= 1 &&
          (int64_t)c->n_pages * c->page < ((int64_t)1 << 31) &&
          // rows of 128 codes are numbered in 32 bits
@@ -185,6 +185,7 @@ int spec_kv8_attention(spec_kv8* h, int layer, const spec_kv8_attention_args* a,
     return fail(h, SPEC_ERR_CAPACITY, "more than %d query heads per kv head", kKv8MaxGroup);
   if (a->dtype != SPEC_DTYPE_BF16 && a->dtype != SPEC_DTYPE_F16)
     return fail(h, SPEC_ERR_ARG, "dtype must be SPEC_DTYPE_BF16 or SPEC_DTYPE_F16");
+  if (a->batch > 65535) return fail(h, SPEC_ERR_CAPACITY, "batch above 65535");
   if (a->max_nodes < 1 || a->max_nodes > kKv8MaxNodes)
     return fail(h, SPEC_ERR_CAPACITY, "max_nodes must be in [1, %d]", kKv8MaxNodes);
   if ((int64_t)a->max_blocks * h->cfg.page >= ((int64_t)1 << 31))

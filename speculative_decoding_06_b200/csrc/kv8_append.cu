@@ -7,7 +7,9 @@
 // exponent; if it grows, the o tokens before the run are multiplied by
 // 2^(e_old - e) and rounded again (exact unless they become subnormal).  The
 // run's values are stored as e4m3(x * 2^-e), rounded to nearest even, infinities
-// saturated to 448: half a step of e4m3, at most 2^-4 of a value.
+// saturated to 448: half a step of e4m3, at most 2^-4 of a value.  A NaN makes its
+// page's exponent byte 255, which reads as NaN and stays until the page is opened
+// anew (place 0): the codes themselves need no NaN, and their readers no test.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -44,7 +46,7 @@ __device__ __forceinline__ void load8(const T* p, float* v) {
   for (int i = 0; i < 8; ++i) v[i] = to_f32<T>(h[i]);
 }
 
-// eight values times `s` as e4m3, round to nearest even, saturating; NaN stays NaN
+// eight values times `s` as e4m3, round to nearest even, saturating
 __device__ __forceinline__ uint2 encode8(const float* v, float s) {
   uint32_t w[4];
 #pragma unroll
@@ -88,6 +90,7 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(Kv8View c, spec_kv
     const int n = run_len;
     const int pg = slot >> c.page_log2;
     float amax = 0.f;
+    bool nan = false;
     for (int r = sub; r < n; r += kRowsAtOnce) {
       float v[8];
       load8(src + row_stride * (a.src_rows ? a.src_rows[i + r] : i + r), v);
@@ -95,19 +98,23 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(Kv8View c, spec_kv
       for (int q = 0; q < 8; ++q) {
         const float m = fabsf(v[q]);
         amax = fmaxf(amax, m < INFINITY ? m : 0.f);
+        nan |= m != m;
       }
     }
-    amax = warp_max(amax);
+    amax = __any_sync(0xffffffffu, nan) ? NAN : warp_max(amax);
     if ((tid & 31) == 0) part[tid >> 5] = amax;
     __syncthreads();
+    nan = isnan(part[2 * plane]) || isnan(part[2 * plane + 1]);
     amax = fmaxf(part[2 * plane], part[2 * plane + 1]);
+    if (!(amax >= 0.f)) amax = 0.f;  // both NaN
     uint8_t* ep = c.exps[plane] + (size_t)pg * c.hkv + head;
     uint8_t* base = c.codes[plane] + (((size_t)pg * c.hkv + head) << c.page_log2) * kKv8Hd + col;
     int e = exponent_of(amax);
     if (place > 0) {
       const int old = (int)*ep - 127;
-      e = max(e, old);
-      if (e > old) {
+      nan |= old == 128;
+      e = nan ? e : max(e, old);
+      if (!nan && e > old) {
         const float f = pow2f(max(old - e, -126));
         for (int r = sub; r < place; r += kRowsAtOnce) {
           uint2* p = reinterpret_cast<uint2*>(base + (size_t)r * kKv8Hd);
@@ -127,7 +134,7 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(Kv8View c, spec_kv
       *reinterpret_cast<uint2*>(base + (size_t)(place + r) * kKv8Hd) = encode8(v, f);
     }
     __syncthreads();  // every thread has read the exponent, `part` and `run_len`
-    if (t == 0) *ep = (uint8_t)(e + 127);
+    if (t == 0) *ep = (uint8_t)(nan ? 255 : e + 127);
     i += n;
   }
 }

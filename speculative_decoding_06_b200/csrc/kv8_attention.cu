@@ -149,8 +149,9 @@ __global__ void __launch_bounds__(kThreads) kv8_decode_kernel(Kv8View c, spec_kv
       const bool ok = pg >= 0 && pg < c.n_pages;
       if (!ok) pg = 0;
       const size_t at = (size_t)pg * c.hkv + kvh;
-      ks = ok ? __int_as_float((int)c.exps[0][at] << 23) : NAN;
-      ve = (float)((int)c.exps[1][at] - 127);
+      const int kb = ok ? c.exps[0][at] : 255, vb = c.exps[1][at];  // 255: NaN
+      ks = kb < 255 ? __int_as_float(kb << 23) : NAN;
+      ve = vb < 255 ? (float)(vb - 127) : NAN;
     }
     s_page[i] = (((pg * c.hkv + kvh) << c.page_log2) + (key & (c.page - 1))) >> 4;
     s_kscale[i] = ks;
@@ -503,9 +504,14 @@ DecodePlan plan_decode(int hkv, int sm_count, int batch, int n_q_heads, int max_
   return p;
 }
 
+bool by_tree(int hkv, int n_q_heads, int max_nodes, int max_prefix) {
+  return max_nodes * (n_q_heads / hkv) > 16 && max_prefix <= kKv8TcMaxChunks * kKv8TcMaxKeys;
+}
+
 }  // namespace
 
 size_t kv8_attention_workspace(const Kv8View& c, int sm_count, int batch, int n_q_heads, int max_nodes, int max_prefix) {
+  if (by_tree(c.hkv, n_q_heads, max_nodes, max_prefix)) return 16;
   int nt = 1;
   size_t bytes = 0;
   plan_decode(c.hkv, sm_count, batch, n_q_heads, max_nodes, max_prefix, &nt, &bytes);
@@ -513,7 +519,7 @@ size_t kv8_attention_workspace(const Kv8View& c, int sm_count, int batch, int n_
 }
 
 cudaError_t kv8_attention_configure() {
-  cudaError_t e = cudaSuccess;
+  cudaError_t e = kv8_tree_configure();
   for (const void* f : {(const void*)kv8_decode_kernel<__nv_bfloat16, 1>, (const void*)kv8_decode_kernel<__nv_bfloat16, 2>,
                         (const void*)kv8_decode_kernel<__half, 1>, (const void*)kv8_decode_kernel<__half, 2>})
     if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::end);
@@ -521,6 +527,7 @@ cudaError_t kv8_attention_configure() {
 }
 
 cudaError_t launch_kv8_attention(const Kv8View& c, const spec_kv8_attention_args& a, int sm_count, cudaStream_t s) {
+  if (by_tree(c.hkv, a.n_q_heads, a.max_nodes, a.max_prefix)) return launch_kv8_tree(c, a, sm_count, s);
   int nt = 1;
   size_t bytes = 0;
   DecodePlan p = plan_decode(c.hkv, sm_count, a.batch, a.n_q_heads, a.max_nodes, a.max_prefix, &nt, &bytes);

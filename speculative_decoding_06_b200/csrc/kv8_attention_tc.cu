@@ -1,0 +1,902 @@
+// Attention over the 8-bit paged cache for draft trees and prompt chunks, on the
+// 5th-generation tensor cores.
+//
+// A CTA holds a tile of 128 query rows (row = node * G + g of one kv head,
+// G = Hq / Hkv) and walks over keys in units of 64, first its share of the cached
+// prefix, then the step's own rows that its rows can see.  Two softmax streams take
+// the units in turn, each with its own running maximum, sum and output; they join
+// at the end.
+//
+//   loader (1 thread)     bulk copies of the codes of a unit, three units deep.
+//   converters (4 warps for K, 4 for V)  turn codes into fp16 (exact) and write them as
+//       the swizzled K and V operands.  K and V of the step's own rows become fp16
+//       times a power of two that their largest value sets.
+//   issuers (1 thread per stream)  S = Q K^T (M 128, N 64) into one of two TMEM buffers and
+//       O += P V (P from TMEM, V MN-major); scores run a unit ahead of products.
+//   softmax (4 warps per stream)  a thread per row: the online softmax in base 2, P as
+//       fp16 over the S that it came from.
+//
+// What bounds it: a unit takes 0.72 us of a CTA, 1350 cycles, of which the MMAs need
+// 512, the exponentials 512 of the special-function units and the conversions 512 of
+// the integer pipe; the rest is the latency of a unit's chain (codes to operand,
+// tensor memory to registers and back, six barriers).  Tried and slower: one issuer for both
+// streams, which keeps them in step, so that both want the special-function units at once (0.95 us);
+// codes by cp.async of the converters (0.95 us); four threads per row, whose exchange of
+// maxima costs what it saves (0.97 us); 128-key score tiles (0.97 us).  Two row tiles
+// that share a unit's conversion took 1.28 us a unit, 11 % less per row, but need twice the
+// rows.  Start and end of a CTA take about 10 us.
+//
+// Scales: the unit's K exponent (the largest of its pages'; codes of a page with a
+// smaller one are multiplied by the difference as they are converted, exact to
+// 2^-33 of the unit's largest value) multiplies the scores; its V exponent w goes
+// into the exponential: p' = 2^(x + w - m) with m a running maximum of x + w that
+// moves only when exceeded by more than 8, O sums p' times bare codes and the
+// denominator p' 2^-w.  p' is rounded to fp16 (2^-11 of itself) for the product only.
+//
+// The CTAs of a cluster share a sequence's prefix evenly and merge their normalised
+// outputs and log-sum-exps through distributed shared memory.
+#include "common.cuh"
+#include "kv8.h"
+
+namespace spec {
+
+namespace {
+
+constexpr int kRowTile = 128;
+constexpr int kKeys = 64;  // keys of a unit
+constexpr int kConvWarps = 4;  // per plane
+constexpr int kConvThreads = 32 * kConvWarps;
+constexpr int kCodeStages = 3;
+constexpr uint32_t kQHalf = kRowTile * 128;  // [128 rows][64 fp16]: 16 KB
+constexpr uint32_t kQTile = 2 * kQHalf;
+constexpr uint32_t kHalf = kKeys * 128;      // [64 keys][64 fp16]: 8 KB
+constexpr uint32_t kUnit = 2 * kHalf;        // one unit's K or V
+constexpr uint32_t kCodeTile = kKeys * kKv8Hd;  // one plane
+constexpr int kMaxUnits = kKv8TcMaxKeys / kKeys;  // of a CTA's share: their pages are looked up up front
+
+constexpr int kRowWarps = 8;  // two streams of four
+constexpr int kIssueWarp = kRowWarps + 2 * kConvWarps;  // and the next one: one per stream
+constexpr int kLoadWarp = kIssueWarp + 2;
+constexpr int kThreads = 32 * (kLoadWarp + 1);
+constexpr int kStages = 4;    // most operand stages of K or V
+
+// mbarriers: per operand stage; S, P and P V per stream and buffer
+enum { B_Q = 0, B_O = 1, B_TREF = 2, B_DRAIN = 4, B_KFULL = 6, B_KEMPTY = B_KFULL + kStages, B_VFULL = B_KEMPTY + kStages,
+       B_VEMPTY = B_VFULL + kStages, B_SFULL = B_VEMPTY + kStages, B_PFULL = B_SFULL + 4, B_PV = B_PFULL + 4,
+       B_CFULL = B_PV + 4, B_CEMPTY = B_CFULL + 2 * kCodeStages, kNumBars = B_CEMPTY + 2 * kCodeStages };
+
+struct M {  // shared memory
+  static constexpr int nk = 3;             // operand stages (units) of K
+  static constexpr int nv = 4;             // and V
+  static constexpr uint32_t q = 0;
+  static constexpr uint32_t k = q + kQTile;
+  static constexpr uint32_t v = k + nk * kUnit;
+  static constexpr uint32_t codes = v + nv * kUnit;
+  static constexpr uint32_t group = codes + 2 * kCodeStages * kCodeTile;  // int4 [kMaxUnits]: first rows / 16 of the groups of 16 keys
+  static constexpr uint32_t kexp = group + 16 * kMaxUnits;                // uint32 [kMaxUnits]: exponent bytes of the four groups
+  static constexpr uint32_t vexp = kexp + 4 * kMaxUnits;
+  static constexpr uint32_t unit = vexp + 4 * kMaxUnits;  // float2 [kMaxUnits + 2]: factor of K, exponent of V
+  static constexpr uint32_t anc = unit + 8 * (kMaxUnits + 2);  // uint64 [2][128][2]
+  static constexpr uint32_t jump = anc + 2 * 128 * 16;    // int [2][128]
+  static constexpr uint32_t row = jump + 2 * 128 * 4;     // float [2][128]: q's factor, at the end the log-sum-exp
+  static constexpr uint32_t red = row + 2 * 128 * 4;      // float [8]: the converter warps' largest K and V values
+  static constexpr uint32_t vbad = red + 32;              // uint32 [4]: own rows whose V holds an infinity or NaN
+  static constexpr uint32_t bars = vbad + 16;
+  static constexpr uint32_t misc = bars + 8 * kNumBars + 8;
+  static constexpr uint32_t end = misc + 16;
+  static constexpr uint32_t dyn = end + 1024;             // to a 1024-byte boundary
+  static constexpr uint32_t stage = q;                    // O, 128 rows x 512 B per stream, over the operands
+};
+static_assert(M::dyn <= 227 * 1024, "shared memory");
+static_assert(M::codes - M::stage >= 2 * 128 * 512, "staging");
+
+// TMEM columns of stream t: two S buffers of 64 at 256 t, O at 256 t + 128.  P lies over the first half of its S.
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kKeys >> 3) << 17) | ((uint32_t)(kRowTile >> 4) << 24);
+constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | ((uint32_t)(128 >> 3) << 17) | ((uint32_t)(kRowTile >> 4) << 24);
+
+struct TcPlan {
+  int chunks;          // CTAs of a cluster
+  uint32_t by_chunks;  // ceil(2^32 / chunks): x / chunks = x * by_chunks >> 32 for x < 2^29
+  uint32_t by_group;   // ceil(2^20 / G): x / G = x * by_group >> 20 for x <= 128 * 64
+};
+
+// `bytes` (a multiple of 16) from global to shared memory, counted on `bar`
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+// the converters of one plane
+__device__ __forceinline__ void sync_converters(int plane) {
+  asm volatile("bar.sync %0, %1;" ::"r"(3 + plane), "n"(kConvThreads) : "memory");
+}
+__device__ __forceinline__ void sync_rows() { asm volatile("bar.sync 2, %0;" ::"n"(32 * kRowWarps) : "memory"); }
+// four e4m3 codes as fp16
+__device__ __forceinline__ void expand4(uint32_t w, uint32_t& x, uint32_t& y) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(x), "=r"(y)
+      : "r"(w));
+}
+// the factor that a page's exponent byte stands for (255: NaN)
+__device__ __forceinline__ float scale_of(int byte) { return byte >= 255 ? NAN : __int_as_float(byte << 23); }
+__device__ __forceinline__ float exp_of(int byte) { return byte >= 255 ? NAN : (float)(byte - 127); }
+__device__ __forceinline__ int max4(uint32_t w) {
+  return max(max((int)(w & 255), (int)(w >> 8 & 255)), max((int)(w >> 16 & 255), (int)(w >> 24)));
+}
+__device__ __forceinline__ float finite_or_0(float x) { return fabsf(x) < INFINITY ? x : 0.f; }
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t mul_h2(uint32_t v, __half2 f) {
+  const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&v), f);
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+// the exponent that brings values up to `amax` below 2^7 (0 where all are 0)
+__device__ __forceinline__ int shift_of(float amax) {
+  const int e = (__float_as_int(amax) >> 23) - 127 - 6;
+  return amax > 0.f ? max(-100, min(120, e)) : 0;
+}
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4& r, float (&v)[8]) {
+  const T* e = reinterpret_cast<const T*>(&r);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = to_f32<T>(e[i]);
+}
+__device__ __forceinline__ uint4 pack8(const float (&v)[8], float f) {
+  return make_uint4(pack2(v[0] * f, v[1] * f), pack2(v[2] * f, v[3] * f), pack2(v[4] * f, v[5] * f),
+                    pack2(v[6] * f, v[7] * f));
+}
+
+// largest magnitude of two 16-bit values' bits (sign cleared), pairwise
+__device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7fff7fffu); }
+template <typename T> __device__ __forceinline__ constexpr uint32_t inf_bits() { return __is_same(T, __half) ? 0x7c00u : 0x7f80u; }
+// sets infinities and NaN among eight 16-bit values to 0; whether there were any
+template <typename T>
+__device__ __forceinline__ bool finite_only(uint4& r) {
+  bool any = false;
+  auto one = [&](uint32_t& w) {
+    const bool lo = (w & 0x7fffu) >= inf_bits<T>(), hi = (w >> 16 & 0x7fffu) >= inf_bits<T>();
+    any |= lo | hi;
+    w &= (lo ? 0u : 0xffffu) | (hi ? 0u : 0xffff0000u);
+  };
+  one(r.x), one(r.y), one(r.z), one(r.w);
+  return any;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_kv8_attention_args a, TcPlan pl) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + M::bars);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + M::misc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + M::misc + 4);
+  int4* s_group = reinterpret_cast<int4*>(smem + M::group);
+  uint32_t* s_vbad = reinterpret_cast<uint32_t*>(smem + M::vbad);
+  float2* s_unit = reinterpret_cast<float2*>(smem + M::unit);
+  float* s_row = reinterpret_cast<float*>(smem + M::row);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = a.n_q_heads / c.hkv;
+  auto by_g = [&](int x) { return (int)((uint32_t)x * pl.by_group >> 20); };
+  // grid: x = row tiles * chunks (a cluster is the chunks of a row tile), y = kv heads, z = batch.  The CTAs of a
+  // cluster differ in `share` only: they return together or not at all
+  const int share = pl.chunks > 1 ? (int)cluster_rank() : 0;
+  const int row0 = (pl.chunks > 1 ? (int)cluster_id_x() : (int)blockIdx.x) * kRowTile;
+  const int b = blockIdx.z, kvh = blockIdx.y;
+  const int first = a.offsets[b], n = a.offsets[b + 1] - first;
+  const int seq = a.seq_ids ? a.seq_ids[b] : b;
+  if (seq < 0 || seq >= a.n_seqs || first < 0 || n < 1 || n > a.max_nodes || n > a.rows - first) return;
+  const int P = a.lengths[seq];
+  const int rows = n * G;
+  if (P < 0 || P > a.max_prefix || row0 >= rows) return;
+  // this CTA's share of the prefix, whole tiles; the last one also has the step's own rows
+  const int per = pl.chunks == 1 ? P : ((int)__umulhi((uint32_t)(P + pl.chunks - 1), pl.by_chunks) + kKeys - 1) / kKeys * kKeys;
+  const int c0 = min(P, share * per), c1 = min(P, c0 + per);
+  const int top = min(n - 1, by_g(row0 + kRowTile - 1));  // last node that a row here can see
+  const int np = (c1 - c0 + kKeys - 1) / kKeys;                   // units of the prefix
+  const int nt = (a.k_new && share == pl.chunks - 1) ? top / kKeys + 1 : 0;  // of the step's own rows: they come last
+  const int nu = np + nt;
+
+  // q: half a warp per row, 16 rows per warp and tile, the first tile's on their way while the pages are looked up
+  uint4 qraw[8];
+  int parent = -1;
+  auto load_q = [&](int tile) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int qr = row0 + kRowTile * tile + 16 * warp + 2 * i + (lane >> 4);
+      const int node = by_g(qr);
+      qraw[i] = make_uint4(0, 0, 0, 0);
+      if (qr < rows)
+        qraw[i] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q) + a.q_row_stride * (first + node) +
+                                                       a.q_head_stride * (kvh * G + (qr - node * G))) + (lane & 15));
+    }
+  };
+  if (warp < kRowWarps) {
+    load_q(0);
+    if (nt > 0 && a.parents && tid <= top) parent = a.parents[first + tid];
+  } else {
+    // pages of the share's units: four groups of 16 keys, each inside one page
+    for (int i = tid - 32 * kRowWarps; i < np; i += kThreads - 32 * kRowWarps) {
+      int pg[4], at[4];
+      uint32_t ke = 0, ve = 0;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int key = c0 + kKeys * i + 16 * u;
+        pg[u] = key < c1 ? a.tables[(size_t)seq * a.max_blocks + (key >> c.page_log2)] : -2;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const bool none = pg[u] == -2, ok = pg[u] >= 0 && pg[u] < c.n_pages;
+        if (!ok) pg[u] = 0;
+        at[u] = pg[u] * c.hkv + kvh;
+        ke |= (none ? 0u : !ok && c0 + kKeys * i + 16 * u < c1 ? 255u : (uint32_t)c.exps[0][at[u]]) << (8 * u);
+        ve |= (none ? 0u : (uint32_t)c.exps[1][at[u]]) << (8 * u);
+        at[u] = ((at[u] << c.page_log2) + ((c0 + kKeys * i + 16 * u) & (c.page - 1))) >> 4;
+      }
+      s_group[i] = make_int4(at[0], at[1], at[2], at[3]);
+      reinterpret_cast<uint32_t*>(smem + M::kexp)[i] = ke;
+      reinterpret_cast<uint32_t*>(smem + M::vexp)[i] = ve;
+      s_unit[i] = make_float2(scale_of(max4(ke)), exp_of(max4(ve)));
+    }
+  }
+  if (warp == kIssueWarp) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    mbar_init(&bar[B_Q], kRowWarps);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&bar[B_KFULL + s], kConvWarps);
+      mbar_init(&bar[B_KEMPTY + s], 1);
+      mbar_init(&bar[B_VFULL + s], kConvWarps);
+      mbar_init(&bar[B_VEMPTY + s], 1);
+    }
+    for (int s = 0; s < 2 * kCodeStages; ++s) {
+      mbar_init(&bar[B_CFULL + s], 1);
+      mbar_init(&bar[B_CEMPTY + s], kConvWarps);
+    }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&bar[B_SFULL + s], 1);
+      mbar_init(&bar[B_PFULL + s], 4);
+      mbar_init(&bar[B_PV + s], 1);
+    }
+    for (int s = 0; s < 2; ++s) mbar_init(&bar[B_TREF + s], 2 * kConvWarps);
+    mbar_init(&bar[B_O], 2);
+    mbar_init(&bar[B_DRAIN], 1);
+    mbar_init(&bar[B_DRAIN + 1], 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (tid < 4) s_vbad[tid] = 0u;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto held = [&](int which, uint32_t parity) { return mbar_wait(&bar[which], parity, nullptr, abort_flag); };
+
+  if (warp == kLoadWarp) {
+    // ------------------------------------------------------------ loads
+    if (elect_one()) {
+      const uint32_t ring = smem_u32(smem + M::codes);
+      bool ok = true;
+      int st = 0, ph = 1, u = 0;
+      for (; u < np && ok; ++u) {
+        const int4 at = s_group[u];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const int sp = p * kCodeStages + st;
+          ok = ok && held(B_CEMPTY + sp, ph);
+          if (!ok) break;
+          uint64_t* full = &bar[B_CFULL + sp];
+          mbar_arrive_expect_tx(full, kCodeTile);
+          const uint32_t dst = ring + sp * kCodeTile;
+          const uint8_t* src = c.codes[p];
+          if (at.y == at.x + 1 && at.z == at.x + 2 && at.w == at.x + 3) {  // one stretch of memory
+            bulk_load(dst, src + (size_t)at.x * (16 * kKv8Hd), kCodeTile, full);
+          } else {
+            bulk_load(dst, src + (size_t)at.x * (16 * kKv8Hd), kCodeTile / 4, full);
+            bulk_load(dst + kCodeTile / 4, src + (size_t)at.y * (16 * kKv8Hd), kCodeTile / 4, full);
+            bulk_load(dst + kCodeTile / 2, src + (size_t)at.z * (16 * kKv8Hd), kCodeTile / 4, full);
+            bulk_load(dst + kCodeTile / 4 * 3, src + (size_t)at.w * (16 * kKv8Hd), kCodeTile / 4, full);
+          }
+        }
+        if (++st == kCodeStages) st = 0, ph ^= 1;
+      }
+      // copies land before the CTA's memory is released: the last into each stage may be under way (a phase that
+      // had none is one that its waiters have seen complete, or never began: the wait then passes or runs out)
+      for (int k = max(0, u - kCodeStages); k < u; ++k)
+        for (int p = 0; p < 2; ++p)
+          mbar_wait(&bar[B_CFULL + p * kCodeStages + k % kCodeStages], (k / kCodeStages) & 1, nullptr, nullptr);
+    }
+    __syncwarp();
+  } else if (warp >= kIssueWarp) {
+    // ------------------------------------------------------------ MMA issue, stream t
+    const int t = warp - kIssueWarp;
+    if (elect_one()) {
+      const uint64_t dq = sw128_kmajor_desc(smem_u32(smem + M::q));
+      const uint64_t dk = sw128_kmajor_desc(smem_u32(smem + M::k));
+      const uint64_t dv = sw128_mnmajor_desc(smem_u32(smem + M::v), kHalf);
+      const uint32_t col = tmem + 256 * t;
+      const int n_own = (nu - t + 1) >> 1;  // units t, t + 2, ...
+      int ks_ = t, kp = 0, vs = t, vp = 0;  // operand stages of K and V, and their phases
+      bool ok = held(B_Q, 0);
+      for (int i = 0; i <= n_own && ok; ++i) {
+        if (i < n_own) {
+          const int sb = 2 * t + (i & 1);
+          // the S buffer holds P of the stream's unit before the last until that one's product is done
+          if (i >= 2) ok = held(B_PV + sb, ((i - 2) >> 1) & 1);
+          ok = ok && held(B_KFULL + ks_, kp);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)  // 16 dimensions per step (a descriptor's low bits count 16 bytes)
+            tc_mma_bf16(col + kKeys * (i & 1), dq + (((ks >> 2) * kQHalf + (ks & 3) * 32) >> 4),
+                        dk + ((ks_ * kUnit + (ks >> 2) * kHalf + (ks & 3) * 32) >> 4), kIdescS, ks > 0 ? 1u : 0u);
+          tc_commit(&bar[B_SFULL + sb]);
+          tc_commit(&bar[B_KEMPTY + ks_]);
+          if ((ks_ += 2) >= M::nk) ks_ -= M::nk, kp ^= 1;
+        }
+        if (i > 0) {  // O += P V of the unit before
+          const int pb = 2 * t + ((i - 1) & 1);
+          ok = held(B_VFULL + vs, vp) && held(B_PFULL + pb, ((i - 1) >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk)  // 16 keys per step: 8 columns of P
+            tc_mma_ts(col + 128, col + kKeys * ((i - 1) & 1) + kk * 8, dv + ((vs * kUnit + kk * 16 * 128) >> 4), kIdescPV,
+                      (i > 1 || kk > 0) ? 1u : 0u);
+          tc_commit(&bar[B_PV + pb]);
+          tc_commit(&bar[B_VEMPTY + vs]);
+          if ((vs += 2) >= M::nv) vs -= M::nv, vp ^= 1;
+        }
+      }
+      if (ok) {
+        tc_commit(&bar[B_O]);
+      } else {
+        *abort_flag = 1;
+        tc_commit(&bar[B_DRAIN + t]);  // issued MMAs finish before the CTA's memory is released
+        mbar_wait(&bar[B_DRAIN + t], 0, nullptr, nullptr);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= kRowWarps) {
+    // ------------------------------------------------------------ converters
+    const int p = (warp - kRowWarps) / kConvWarps;  // 0: K, 1: V
+    const int x = tid - 32 * kRowWarps - p * kConvThreads;
+    // 16 dimensions (piece ch) of keys kr, + 16, + 32, + 48 of a unit: eight lanes have eight keys and eight pieces,
+    // which meet in no bank, neither where the codes lie in rows of 128 bytes nor in the swizzled operands
+    const int wv = x >> 5, kr = (wv >> 1) * 8 + (lane & 7), ch = ((lane >> 3) + 4 * (wv & 1) + lane) & 7;
+    uint8_t* const op0 = smem + (p ? M::v : M::k) + (ch >> 2) * kHalf + kr * 128;
+    const uint32_t col0 = ((2 * (ch & 3)) ^ (kr & 7)) << 4, col1 = ((2 * (ch & 3) + 1) ^ (kr & 7)) << 4;
+    bool ok = true;
+    // operand stages in turn; one is free once the MMAs that read its last unit are done
+    const int n_stages = p ? M::nv : M::nk;
+    int st = 0, ph = 1;
+    auto enter = [&]() {
+      if (ok) ok = held((p ? B_VEMPTY : B_KEMPTY) + st, ph);  // (the first round's waits pass at once)
+      ok = __all_sync(0xffffffffu, ok);
+      return op0 + st * kUnit;
+    };
+    auto arrive = [&]() {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[(p ? B_VFULL : B_KFULL) + st]);
+      if (++st == n_stages) st = 0, ph ^= 1;
+    };
+    const uint32_t* const s_exp = reinterpret_cast<const uint32_t*>(smem + (p ? M::vexp : M::kexp));
+    // the step's own rows, 64 nodes per tile: their largest finite value sets the tile's exponent
+    const T* const own = reinterpret_cast<const T*>(p ? a.v_new : a.k_new) +
+                         (p ? a.v_head_stride : a.k_head_stride) * kvh + 16 * ch;
+    const int64_t own_stride = p ? a.v_row_stride : a.k_row_stride;
+    auto own_row = [&](int tt, int u, uint4 (&raw)[2]) {
+      const int node = kKeys * tt + 16 * u + kr;
+      raw[0] = raw[1] = make_uint4(0, 0, 0, 0);
+      if (node <= top) {
+        const uint4* at = reinterpret_cast<const uint4*>(own + own_stride * (first + node));
+        raw[0] = __ldg(at);
+        raw[1] = __ldg(at + 1);
+      }
+    };
+    for (int tt = 0; tt < nt; ++tt) {
+      uint4 raw[4][2];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) own_row(tt, u, raw[u]);
+      uint32_t big = 0;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const uint4 r = raw[u >> 1][u & 1];
+        big = max_abs2(max_abs2(max_abs2(max_abs2(big, r.x), r.y), r.z), r.w);
+      }
+      if (max(big & 0xffffu, big >> 16) >= inf_bits<T>()) {  // (rare) infinities or NaN
+        big = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          bool wild = false;
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) wild |= finite_only<T>(raw[u][hh]);
+          big = max_abs2(max_abs2(max_abs2(max_abs2(big, raw[u][0].x), raw[u][0].y), raw[u][0].z), raw[u][0].w);
+          big = max_abs2(max_abs2(max_abs2(max_abs2(big, raw[u][1].x), raw[u][1].y), raw[u][1].z), raw[u][1].w);
+          const int node = kKeys * tt + 16 * u + kr;
+          if (p && wild) atomicOr(&s_vbad[node >> 5], 1u << (node & 31));
+        }
+      }
+      big = __reduce_max_sync(0xffffffffu, max(big & 0xffffu, big >> 16));
+      uint32_t* red = reinterpret_cast<uint32_t*>(smem + M::red) + kConvWarps * p;
+      if (lane == 0) red[x >> 5] = big;
+      sync_converters(p);
+#pragma unroll
+      for (int w = 0; w < kConvWarps; ++w) big = max(big, red[w]);
+      const uint16_t top_bits = (uint16_t)big;
+      const int shift = shift_of(to_f32<T>(*reinterpret_cast<const T*>(&top_bits)));
+      if (x == 0) (&s_unit[np + tt].x)[p] = p ? (float)shift : pow2i(shift);
+      sync_converters(p);  // (also: everyone has read `red`)
+      if (lane == 0) mbar_arrive(&bar[B_TREF + tt]);
+    }
+    const uint8_t* const codes = smem + M::codes + p * (kCodeStages * kCodeTile) + kr * kKv8Hd + 16 * ch;
+    int cs = 0, cp = 0;  // stage of the codes, its phase
+    for (int j = 0; j < np; ++j) {
+      if (ok) ok = held(B_CFULL + p * kCodeStages + cs, cp);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      uint4 w[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) w[u] = *reinterpret_cast<const uint4*>(codes + cs * kCodeTile + u * (16 * kKv8Hd));
+      if (p && j == np - 1) {  // what lies behind the sequence's end may be anything; 0 * NaN would spread
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (c0 + kKeys * j + 16 * u + kr >= c1) w[u] = make_uint4(0, 0, 0, 0);
+      }
+      const uint32_t e4 = s_exp[j];
+      uint8_t* const op = enter();
+      if (!ok) break;
+      if (e4 == __byte_perm(e4, 0, 0)) {  // pages of one scale
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          uint4 lo, hi;
+          expand4(w[u].x, lo.x, lo.y);
+          expand4(w[u].y, lo.z, lo.w);
+          expand4(w[u].z, hi.x, hi.y);
+          expand4(w[u].w, hi.z, hi.w);
+          *reinterpret_cast<uint4*>(op + 2048 * u + col0) = lo;
+          *reinterpret_cast<uint4*>(op + 2048 * u + col1) = hi;
+        }
+      } else {
+        const int ref = max4(e4);
+#pragma unroll 1
+        for (int u = 0; u < 4; ++u) {
+          const int d = ref - (int)(e4 >> (8 * u) & 255);
+          const __half2 f = __float2half2_rn(d > 24 ? 0.f : pow2i(-d));
+          const uint4 y = u == 0 ? w[0] : u == 1 ? w[1] : u == 2 ? w[2] : w[3];
+          uint4 lo, hi;
+          expand4(y.x, lo.x, lo.y);
+          expand4(y.y, lo.z, lo.w);
+          expand4(y.z, hi.x, hi.y);
+          expand4(y.w, hi.z, hi.w);
+          *reinterpret_cast<uint4*>(op + 2048 * u + col0) =
+              make_uint4(mul_h2(lo.x, f), mul_h2(lo.y, f), mul_h2(lo.z, f), mul_h2(lo.w, f));
+          *reinterpret_cast<uint4*>(op + 2048 * u + col1) =
+              make_uint4(mul_h2(hi.x, f), mul_h2(hi.y, f), mul_h2(hi.z, f), mul_h2(hi.w, f));
+        }
+      }
+      arrive();
+      if (lane == 0) mbar_arrive(&bar[B_CEMPTY + p * kCodeStages + cs]);  // (all lanes have read theirs: arrive() syncs)
+      if (++cs == kCodeStages) cs = 0, cp ^= 1;
+    }
+    for (int tt = 0; tt < nt && ok; ++tt) {
+      const int j = np + tt;
+      uint8_t* const op = enter();
+      if (!ok) break;
+      const float2 e = s_unit[j];
+      const float f = p ? pow2i(-(int)e.y) : 1.f / e.x;  // (powers of two)
+      // V's infinities and NaN become 0, because 0 * NaN would reach rows that do not see them; they are added at
+      // the end
+      const bool wild = p && (s_vbad[2 * tt] | s_vbad[2 * tt + 1]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        uint4 raw[2];
+        own_row(tt, u, raw);
+        if (wild) {
+          finite_only<T>(raw[0]);
+          finite_only<T>(raw[1]);
+        }
+        float v[8];
+        unpack8<T>(raw[0], v);
+        *reinterpret_cast<uint4*>(op + 2048 * u + col0) = pack8(v, f);
+        unpack8<T>(raw[1], v);
+        *reinterpret_cast<uint4*>(op + 2048 * u + col1) = pack8(v, f);
+      }
+      arrive();
+    }
+    if (!ok) *abort_flag = 1;
+  } else {
+    // ------------------------------------------------------------ softmax rows
+    const int t = warp >> 2;                 // stream
+    const int r = (warp & 3) * 32 + lane;    // TMEM lane
+    const int qr = row0 + r;
+    const bool row_ok = qr < rows;
+    const int node = row_ok ? by_g(qr) : 0;
+    const bool warp_on = __any_sync(0xffffffffu, row_ok);
+    // q as fp16: bf16 rows times a power of two (see shift_of)
+    // (rolled up: code that runs once costs its instruction fetches)
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+      const int qrow = 16 * warp + 2 * i + (lane >> 4);
+      int ex = 0;
+      uint4 y = qraw[0];
+#pragma unroll
+      for (int k = 0; k < 7; ++k) qraw[k] = qraw[k + 1];
+      if (!__is_same(T, __half)) {
+        float v[8];
+        unpack8<T>(y, v);
+        float m = 0.f;
+#pragma unroll
+        for (int q = 0; q < 8; q += 2) m = fmaxf(m, fmaxf(fabsf(v[q]), fabsf(v[q + 1])));  // (NaN is passed over)
+        if (m == INFINITY) {  // the largest of the finite values
+          m = 0.f;
+#pragma unroll 1
+          for (int q = 0; q < 8; ++q) m = fmaxf(m, fabsf(finite_or_0(to_f32<T>(reinterpret_cast<const T*>(&y)[q]))));
+        }
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        ex = shift_of(m);
+        y = pack8(v, pow2i(-ex));
+      }
+      *reinterpret_cast<uint4*>(smem + M::q + ((lane >> 3) & 1) * kQHalf + qrow * 128 +
+                                (((lane & 7) ^ (qrow & 7)) << 4)) = y;
+      if ((lane & 15) == 0) s_row[qrow] = a.scale * 1.4426950408889634f * pow2i(ex);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar[B_Q]);
+    // ancestors: each node's set doubles its reach per round (128 nodes: seven rounds)
+    uint64_t anc0 = 0, anc1 = 0;
+    {
+      ulonglong2* set = reinterpret_cast<ulonglong2*>(smem + M::anc);
+      int* jump = reinterpret_cast<int*>(smem + M::jump);
+      if (nt > 0 && a.parents && tid < 128) {
+        set[tid] = make_ulonglong2(tid < 64 ? 1ull << tid : 0ull, tid < 64 ? 0ull : 1ull << (tid - 64));
+        jump[tid] = parent < tid && parent >= 0 ? parent : -1;
+      }
+      sync_rows();
+      int cur = 0;
+      if (nt > 0 && a.parents) {
+        for (int reach = 1; reach <= top; reach *= 2) {
+          if (tid < 128) {
+            ulonglong2 s = set[cur * 128 + tid];
+            int up = jump[cur * 128 + tid];
+            if (up >= 0) {
+              const ulonglong2 s2 = set[cur * 128 + up];
+              s.x |= s2.x;
+              s.y |= s2.y;
+              up = jump[cur * 128 + up];
+            }
+            set[(cur ^ 1) * 128 + tid] = s;
+            jump[(cur ^ 1) * 128 + tid] = up;
+          }
+          cur ^= 1;
+          sync_rows();
+        }
+      }
+      if (nt > 0) {
+        if (a.parents) {
+          anc0 = set[cur * 128 + node].x;
+          anc1 = set[cur * 128 + node].y;
+        } else {
+          anc0 = node >= 63 ? ~0ull : (2ull << node) - 1;
+          anc1 = node < 64 ? 0 : node >= 127 ? ~0ull : (2ull << (node - 64)) - 1;
+        }
+      }
+    }
+    const float qs = s_row[r];
+    const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256 * t;  // this warp's lanes, the stream's columns
+    const int n_own = (nu - t + 1) >> 1;  // the stream's units
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+#pragma unroll 1
+    for (int i = 0; i < n_own; ++i) {
+      const int u = 2 * i + t, sb = 2 * t + (i & 1);
+      const uint32_t ts = tl + kKeys * (i & 1);
+      uint64_t see = ~0ull;  // keys of the unit that the row sees
+      if (u >= np - 1) {
+        if (u >= np) {
+          if (ok) ok = held(B_TREF + u - np, 0);
+          see = u == np ? anc0 : anc1;
+        } else {
+          const int left = c1 - (c0 + kKeys * u);
+          if (left < kKeys) see = (1ull << left) - 1;
+        }
+      }
+      const float2 e = s_unit[u];
+      const float f = qs * e.x, ve = e.y;
+      const float un = fast_exp2(-ve);
+      if (ok) ok = held(B_SFULL + sb, (i >> 1) & 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok && warp_on) {
+        tc_fence_after();
+        // twice through the scores, 32 at a time: the largest first
+        const bool masked = __any_sync(0xffffffffu, see != ~0ull);
+        auto scores = [&](int c, uint32_t (&s)[32]) {
+          tmem_ld32_async(ts + 32 * c, s);
+          tmem_wait_ld();
+          tmem_reg_fence32(s);
+          if (masked) {
+            const uint32_t w = (uint32_t)(see >> (32 * c));
+#pragma unroll
+            for (int q = 0; q < 32; ++q) s[q] = (w >> q & 1u) ? s[q] : 0xff800000u;
+          }
+        };
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t s[32];
+          scores(c, s);
+          float m0 = __uint_as_float(s[0]), m1 = __uint_as_float(s[1]);
+#pragma unroll
+          for (int q = 2; q < 30; q += 4) {
+            m0 = fmax3(m0, __uint_as_float(s[q]), __uint_as_float(s[q + 1]));
+            m1 = fmax3(m1, __uint_as_float(s[q + 2]), __uint_as_float(s[q + 3]));
+          }
+          mx = fmax3(mx, fmax3(m0, __uint_as_float(s[30]), __uint_as_float(s[31])), m1);
+        }
+        mx = fmaf(mx, f, ve);
+        const bool up = mx > m + 8.f;
+        if (__any_sync(0xffffffffu, up)) {
+          const float keep = up ? fast_exp2(m - mx) : 1.f;
+          m = up ? mx : m;
+          l *= keep;
+          if (i > 0) {
+            // O shrinks: the product of the stream's last unit has to be in it
+            ok = __all_sync(0xffffffffu, held(B_PV + (sb ^ 1), ((i - 1) >> 1) & 1));
+            if (ok) {
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < 8; ++c) {
+                float o[16];
+                tmem_ld16(tl + 128 + 16 * c, o);
+#pragma unroll
+                for (int q = 0; q < 16; ++q) o[q] *= keep;
+                tmem_st16_async(tl + 128 + 16 * c, reinterpret_cast<const uint32_t*>(o));
+              }
+              tmem_wait_st();
+            }
+          }
+        }
+        const float add = ve - (m == -INFINITY ? 0.f : m);
+        const uint64_t f2 = f2_pack(f, f), a2 = f2_pack(add, add);
+        uint64_t l0 = f2_pack(0.f, 0.f), l1 = l0;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t s[32], p[16];
+          scores(c, s);
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            float y0, y1;
+            f2_unpack(f2_fma(u2_pack(s[2 * q], s[2 * q + 1]), f2, a2), y0, y1);
+            y0 = fast_exp2(y0);
+            y1 = fast_exp2(y1);
+            if (q & 1) l1 = f2_add(l1, f2_pack(y0, y1));
+            else l0 = f2_add(l0, f2_pack(y0, y1));
+            p[q] = pack2(y0, y1);
+          }
+          tmem_st16_async(ts + 16 * c, p);  // over scores that have been read
+        }
+        float s0, s1;
+        f2_unpack(f2_add(l0, l1), s0, s1);
+        l = fmaf(s0 + s1, un, l);
+        tmem_wait_st();
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[B_PFULL + sb]);
+    }
+    if (ok && nu > 0) ok = held(B_O, 0);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) *abort_flag = 1;
+    // normalised output of this stream; two streams of the same rows join in the first one.  It is written out, or
+    // staged over operands that are done with (B_O follows every MMA) where a cluster shares the prefix.
+    float inv = !ok ? NAN : l == 0.f ? 0.f : 1.f / l;
+    float lse = !ok ? NAN : l == 0.f ? -INFINITY : m + log2f(l);
+    const bool o_on = ok && n_own > 0;  // (uniform: else O was never written)
+    if (o_on) tc_fence_after();
+    const uint32_t sw = (uint32_t)(r & 7) << 4;
+    uint8_t* const stg0 = smem + M::stage + r * 512;
+    uint8_t* const stg1 = stg0 + 128 * 512;
+    auto read_o = [&](int c, float (&o)[16]) {
+      if (o_on) {
+        tmem_ld16(tl + 128 + 16 * c, o);
+#pragma unroll
+        for (int q = 0; q < 16; ++q) o[q] *= inv;
+      } else {
+#pragma unroll
+        for (int q = 0; q < 16; ++q) o[q] = ok ? 0.f : NAN;
+      }
+    };
+    auto stage_o = [&](uint8_t* stg, int c, const float (&o)[16]) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<float4*>(stg + (((4 * c + q) << 4) ^ sw)) =
+            make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+    };
+    float w1 = 0.f;
+    if (t == 1) {
+      if (warp_on) {
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          float o[16];
+          read_o(c, o);
+          stage_o(stg1, c, o);
+        }
+      }
+      s_row[kRowTile + r] = lse;
+    }
+    sync_rows();
+    if (t == 0) {
+      const float other = s_row[kRowTile + r], mx = fmaxf(lse, other);
+      const float a0 = lse == -INFINITY ? 0.f : fast_exp2(lse - mx), a1 = other == -INFINITY ? 0.f : fast_exp2(other - mx);
+      const float sum = a0 + a1, is = sum == 0.f ? 0.f : 1.f / sum;
+      inv *= a0 * is;
+      w1 = a1 * is;
+      lse = sum == 0.f ? -INFINITY : mx + log2f(sum);
+    }
+    if (warp_on && t == 0) {
+      const bool wild = nt > 0 && (s_vbad[0] | s_vbad[1] | s_vbad[2] | s_vbad[3]);
+      T* out = reinterpret_cast<T*>(a.out) + a.out_row_stride * (first + node) + (size_t)(kvh * G + (qr - node * G)) * kKv8Hd;
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
+        float o[16];
+        read_o(c, o);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float4 y = *reinterpret_cast<const float4*>(stg1 + (((4 * c + q) << 4) ^ sw));
+          o[4 * q] = fmaf(w1, y.x, o[4 * q]);
+          o[4 * q + 1] = fmaf(w1, y.y, o[4 * q + 1]);
+          o[4 * q + 2] = fmaf(w1, y.z, o[4 * q + 2]);
+          o[4 * q + 3] = fmaf(w1, y.w, o[4 * q + 3]);
+        }
+        if (wild && row_ok) {  // infinities and NaN in V of the step's own rows, for the rows that see them
+#pragma unroll 1
+          for (int k = 0; k <= top; ++k) {
+            if (!(s_vbad[k >> 5] >> (k & 31) & 1u)) continue;
+            if (!((k < 64 ? anc0 >> k : anc1 >> (k - 64)) & 1)) continue;
+            const T* vp = reinterpret_cast<const T*>(a.v_new) + a.v_row_stride * (first + k) + a.v_head_stride * kvh + 16 * c;
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+              const float v = to_f32<T>(vp[q]);
+              if (!(fabsf(v) < INFINITY)) o[q] += v;
+            }
+          }
+        }
+        if (pl.chunks == 1) {
+          if (row_ok) {
+            uint4 w[2];
+            T* e = reinterpret_cast<T*>(w);
+#pragma unroll
+            for (int q = 0; q < 16; ++q) e[q] = from_f32<T>(o[q]);
+            reinterpret_cast<uint4*>(out + 16 * c)[0] = w[0];
+            reinterpret_cast<uint4*>(out + 16 * c)[1] = w[1];
+          }
+        } else {
+          stage_o(stg0, c, o);
+        }
+      }
+      if (pl.chunks > 1) s_row[r] = lse;
+      else if (row_ok && a.lse)
+        a.lse[(size_t)(first + node) * a.n_q_heads + kvh * G + (qr - node * G)] = lse * 0.69314718055994531f;
+    }
+  }
+
+  if (pl.chunks > 1) {
+    // merge: every CTA of the cluster writes a slice of the rows, from all CTAs' parts of them
+    cluster_sync_all();
+    const int valid = min(kRowTile, rows - row0);
+    const int per_cta = (int)__umulhi((uint32_t)(valid + pl.chunks - 1), pl.by_chunks);
+    const int rb = share * per_cta, re = min(valid, rb + per_cta);
+    const uint32_t row_base = smem_u32(s_row), stage_base = smem_u32(smem + M::stage);
+    static_assert(kKv8TcMaxChunks == 8, "two loads of four parts");
+    for (int rr = rb + warp; rr < re; rr += kThreads / 32) {
+      const int q2 = row0 + rr, node = by_g(q2);
+      const uint32_t soff = stage_base + (uint32_t)(rr * 512 + ((lane ^ (rr & 7)) << 4));
+      // lane k has part k's log-sum-exp
+      float x = -INFINITY;
+      if (lane < pl.chunks) x = dsmem_ld_f32(map_peer(row_base + 4 * rr, lane));
+      float4 y[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) y[k] = dsmem_ld_f4(map_peer(soff, min(k, pl.chunks - 1)));
+      float mx = x;
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      float w = x == -INFINITY ? 0.f : fast_exp2(x - mx);
+      float sum = w;
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      w *= sum == 0.f ? 0.f : 1.f / sum;
+      if (a.lse && lane == 0)
+        a.lse[(size_t)(first + node) * a.n_q_heads + kvh * G + (q2 - node * G)] =
+            sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994531f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k0 = 0; k0 < 8; k0 += 4) {
+        if (k0 && pl.chunks <= 4) break;
+        if (k0) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) y[k] = dsmem_ld_f4(map_peer(soff, min(k0 + k, pl.chunks - 1)));
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float wk = __shfl_sync(0xffffffffu, w, k0 + k);  // (0 beyond the last part)
+          acc = make_float4(fmaf(wk, y[k].x, acc.x), fmaf(wk, y[k].y, acc.y), fmaf(wk, y[k].z, acc.z), fmaf(wk, y[k].w, acc.w));
+        }
+      }
+      T e[4] = {from_f32<T>(acc.x), from_f32<T>(acc.y), from_f32<T>(acc.z), from_f32<T>(acc.w)};
+      *reinterpret_cast<uint2*>(reinterpret_cast<T*>(a.out) + a.out_row_stride * (first + node) +
+                                (size_t)(kvh * G + (q2 - node * G)) * kKv8Hd + 4 * lane) = *reinterpret_cast<const uint2*>(e);
+    }
+  }
+  tc_fence_before();
+  if (pl.chunks > 1) cluster_sync_all();  // no CTA leaves while a peer reads it
+  else __syncthreads();
+  if (warp == kIssueWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <typename T>
+cudaError_t launch_tree(const Kv8View& c, const spec_kv8_attention_args& a, const TcPlan& p, int row_tiles,
+                        cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.chunks * row_tiles, c.hkv, a.batch);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = M::dyn;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.chunks;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.chunks > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kv8_tree_kernel<T>, c, a, p);
+}
+
+template <typename T>
+cudaError_t configure_tree() {
+  cudaError_t e = cudaFuncSetAttribute(kv8_tree_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)M::dyn);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kv8_tree_kernel<T>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             (int)cudaSharedmemCarveoutMaxShared);
+  return e;
+}
+
+}  // namespace
+
+cudaError_t kv8_tree_configure() {
+  cudaError_t e = configure_tree<__nv_bfloat16>();
+  return e == cudaSuccess ? configure_tree<__half>() : e;
+}
+
+cudaError_t launch_kv8_tree(const Kv8View& c, const spec_kv8_attention_args& a, int sm_count, cudaStream_t s) {
+  const int G = a.n_q_heads / c.hkv;
+  const int row_tiles = (a.max_nodes * G + kRowTile - 1) / kRowTile;
+  const long long tiles = (long long)a.batch * c.hkv * row_tiles;
+  const int units = (a.max_prefix + kKeys - 1) / kKeys;
+  // A cluster shares a prefix only while SMs would idle, and a share is at least eight units: joining shares takes
+  // 4 us, as long as five units (one tree of 61 nodes, 2048 tokens, 16 tiles: 32 us with one CTA each, 26, 20 and 21
+  // with 2, 4 and 6; 256 tiles of 512 - 4096 tokens: 83 us with one, 95 with two)
+  long long chunks = tiles > sm_count ? 1 : sm_count / tiles;
+  chunks = chunks < units / 8 ? chunks : units / 8;
+  chunks = chunks < 1 ? 1 : chunks > kKv8TcMaxChunks ? kKv8TcMaxChunks : chunks;
+  const int need = (a.max_prefix + kKv8TcMaxKeys - 1) / kKv8TcMaxKeys;
+  TcPlan p;
+  p.chunks = chunks < need ? need : (int)chunks;
+  p.by_chunks = (uint32_t)((((uint64_t)1 << 32) + p.chunks - 1) / p.chunks);
+  p.by_group = (uint32_t)(((1u << 20) + G - 1) / G);
+  return a.dtype == SPEC_DTYPE_BF16 ? launch_tree<__nv_bfloat16>(c, a, p, row_tiles, s)
+                                    : launch_tree<__half>(c, a, p, row_tiles, s);
+}
+
+}  // namespace spec

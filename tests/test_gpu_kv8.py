@@ -15,7 +15,7 @@ DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "f32": torch.float32}
 
 
 def make_cache(n_pages, hkv, page, layers=1, garbage=None):
-    """A cache whose memory holds `garbage` (0x7F: e4m3's NaN) until it is written."""
+    """A cache whose memory holds `garbage` until it is written (0x7F: e4m3's NaN, and an exponent of 0)."""
     from speculative_decoding_06_b200.kv8 import KV8Cache
     cache = KV8Cache(layers, hkv, n_pages, page)
     if garbage is not None:
@@ -139,9 +139,11 @@ def check_append(cache, k, v, slots, src=None):
     cache.append(0, k, v, i32(slots), None if src is None else i32(src))
     got_e, got_c = cache.exps.cpu().numpy(), cache.codes.cpu().numpy()
     assert np.array_equal(got_e, exps)
-    same = got_c == codes
-    nan = np.isnan(O.E4M3[got_c]) & np.isnan(O.E4M3[codes])  # NaN of either sign
-    assert (same | nan).all()
+    # the codes of a page that holds NaN are unspecified; nothing else of the cache may have changed
+    assert np.array_equal(got_c[exps < 255], codes[exps < 255])
+    touched = np.zeros(exps.shape[2], bool)
+    touched[[s // cache.page for s in slots if 0 <= s < cache.page * cache.n_pages]] = True
+    assert np.array_equal(got_c[:, :, ~touched], codes[:, :, ~touched])
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "f32"])
@@ -352,7 +354,7 @@ def test_attention_bad_descriptions_reach_no_other_entry(nodes, hq):
     assert (out[o[2]:] == 7).all() and (lse[o[2]:] == 7).all()
 
 
-@pytest.mark.parametrize("n", [5, 61])
+@pytest.mark.parametrize("n", [5, 61, 128])
 def test_attention_nonfinite_values_reach_only_the_rows_that_see_them(n):
     c = attention_case(15, [70], [n], 4, 1, 64, "bf16")
     c["v"][3, 0, 5], c["v"][3, 0, 6], c["v"][4, 0, 7] = math.inf, math.nan, -math.inf
@@ -370,14 +372,18 @@ def test_attention_nonfinite_values_reach_only_the_rows_that_see_them(n):
     assert np.allclose(out[part], want[part], rtol=0.02, atol=0.02)
 
 
-def test_attention_nan_in_the_prefix():
-    c = attention_case(16, [70, 70], [3, 20], 2, 1, 16, "fp16")
-    c["codes"][1, c["tables"][c["ids"][0], 2], 0, 3, 17] = 0x7F
-    c["cache"].codes[0] = torch.from_numpy(c["codes"])
+@pytest.mark.parametrize("plane", [0, 1])
+@pytest.mark.parametrize("nodes", [[3, 2], [61, 30]])
+def test_attention_nan_page_reaches_its_sequence_and_head_only(plane, nodes):
+    c = attention_case(16, [70, 70], nodes, 4, 2, 16, "fp16")
+    c["exps"][plane, c["tables"][c["ids"][0], 2], 1] = 255
+    c["cache"].exps[0] = torch.from_numpy(c["exps"])
     got, ref = run_attention(c), reference(c)
-    out = got[0].double().cpu().numpy()
-    assert np.array_equal(np.isnan(out), np.isnan(ref[0])) and np.isnan(out[:3, :, 17]).all()
-    assert not np.isnan(out[3:]).any() and not np.isnan(out[:3, :, 16]).any()
+    out, n = got[0].double().cpu().numpy(), nodes[0]
+    assert np.isnan(ref[0][:n, 2:]).all() and np.isnan(out[:n, 2:]).all()
+    assert not np.isnan(out[:n, :2]).any() and not np.isnan(out[n:]).any()
+    check_attention(c, (got[0][n:], got[1][n:]), [x[n:] for x in ref])
+    check_attention(c, (got[0][:n, :2], got[1][:n, :2]), [x[:n, :2] for x in ref])
 
 
 def test_refusals_of_the_torch_side():
