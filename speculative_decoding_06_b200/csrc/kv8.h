@@ -26,6 +26,7 @@ struct Kv8View {
   uint8_t* codes[2];  // K, V: [page id][kv head][token][128]
   uint8_t* exps[2];   // K, V: [page id][kv head]
   int n_pages, page, page_log2, hkv;
+  int row0[2];        // first row (of 128 codes) of each plane in the whole cache
 };
 
 cudaError_t kv8_plan_configure();
@@ -33,7 +34,7 @@ cudaError_t launch_kv8_plan(const spec_kv8_plan_args& a, int page_log2, int n_pa
 cudaError_t launch_kv8_append(const Kv8View& c, const spec_kv8_append_args& a, int sm_count, cudaStream_t s);
 cudaError_t kv8_attention_configure();
 size_t kv8_attention_workspace(const Kv8View& c, int sm_count, int batch, int n_q_heads, int max_nodes, int max_prefix);
-cudaError_t launch_kv8_attention(const Kv8View& c, const spec_kv8_attention_args& a, int sm_count, cudaStream_t s);
+cudaError_t launch_kv8_attention(const Kv8View& c, const CUtensorMap& map, const spec_kv8_attention_args& a, int sm_count, cudaStream_t s);
 
 // rows > 16 per kv head: the tensor-core kernel (prefixes up to kKv8TcMaxChunks * kKv8TcMaxKeys; no workspace)
 cudaError_t kv8_tree_configure();

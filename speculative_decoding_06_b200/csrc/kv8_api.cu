@@ -20,6 +20,7 @@ struct spec_kv8 {
   int device = 0;
   int sm_count = 148;
   int page_log2 = 4;
+  CUtensorMap map;  // the codes as rows of 128 bytes, boxes of 16 rows, 128-byte swizzle
   char err[256] = "";
 };
 
@@ -74,11 +75,31 @@ Kv8View view_of(const spec_kv8* h, int layer) {
     v.codes[p] = h->codes + (2 * (size_t)layer + p) * cp;
     v.exps[p] = h->exps + (2 * (size_t)layer + p) * ep;
   }
+  for (int p = 0; p < 2; ++p) v.row0[p] = (int)((2 * (size_t)layer + p) * ep * c.page);
   v.n_pages = c.n_pages;
   v.page = c.page;
   v.page_log2 = h->page_log2;
   v.hkv = c.n_kv_heads;
   return v;
+}
+
+bool encode_map(CUtensorMap* m, void* codes, uint64_t rows) {
+  typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+      q != cudaDriverEntryPointSuccess)
+    return false;
+  const cuuint64_t dims[2] = {kKv8Hd, rows};
+  const cuuint64_t strides[1] = {kKv8Hd};
+  const cuuint32_t box[2] = {kKv8Hd, 16};
+  const cuuint32_t estr[2] = {1, 1};
+  return reinterpret_cast<EncodeTiledFn>(p)(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, codes, dims, strides, box, estr,
+                                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                            CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int launched(spec_kv8* h, cudaError_t e, const char* what) {
@@ -113,6 +134,10 @@ int spec_kv8_open(const spec_kv8_config* cfg, void* codes, size_t code_bytes, vo
   }
   spec_kv8* h = new (std::nothrow) spec_kv8;
   if (!h) return SPEC_ERR_CAPACITY;
+  if (dev >= 0 && !encode_map(&h->map, codes, (uint64_t)spec_kv8_code_bytes(cfg) / kKv8Hd)) {
+    delete h;
+    return SPEC_ERR_CUDA;
+  }
   h->cfg = *cfg;
   h->codes = static_cast<uint8_t*>(codes);
   h->exps = static_cast<uint8_t*>(exps);
@@ -210,7 +235,7 @@ int spec_kv8_attention(spec_kv8* h, int layer, const spec_kv8_attention_args* a,
   if (int rc = check_device(h)) return rc;
   spec_kv8_attention_args b = *a;
   if (b.scale == 0.f) b.scale = 0.08838834764831845f;  // 1 / sqrt(128)
-  return launched(h, launch_kv8_attention(view_of(h, layer), b, h->sm_count, static_cast<cudaStream_t>(cuda_stream)),
+  return launched(h, launch_kv8_attention(view_of(h, layer), h->map, b, h->sm_count, static_cast<cudaStream_t>(cuda_stream)),
                   "attention");
 }
 

@@ -8,9 +8,9 @@
 // codes in registers:
 //
 //   scores   S^T = K Q^T by mma.m16n8k16: 16 keys by 8 rows.  The contraction's
-//            order is free, so lane (g, t) takes dimensions 16t.. and 64+16t.. of
-//            keys g and g + 8: whole 16-byte pieces, each word of codes (4 dims)
-//            one k-step's two A registers after e4m3 -> fp16 conversion (exact).
+//            order is free, so lane (g, t) takes dimensions 32t .. 32t + 31 of keys
+//            g and g + 8: whole 16-byte pieces, each word of codes (4 dims) one
+//            k-step's two A registers after e4m3 -> fp16 conversion (exact).
 //   softmax  in 32 bits, base 2, with a running maximum per row.  A page's K
 //            scale multiplies the scores; its V scale 2^w goes into the
 //            exponent: p' = 2^(x + w - m), m the running maximum of x + w, so
@@ -20,9 +20,11 @@
 //            2t+1, 2t+8, 2t+9; two keys' bytes interleave into A registers;
 //            the scores' accumulators become the B operand by movmatrix.
 //
-// Each warp streams tiles of 32 keys through a private queue in shared memory
-// that it fills with cp.async (every thread reads only what it copied itself: no
-// barrier), three tiles deep.  The step's own rows (16-bit K and V) are added by
+// Each warp streams tiles of 32 keys through a queue of its own in shared memory,
+// three tiles deep, which one lane fills by TMA (boxes of 16 keys, each inside one
+// page; the 128-byte swizzle keeps both products' reads free of bank conflicts).
+// Sixteen cp.async per lane and tile instead took longer to issue than the rest of
+// the tile (89 us for a batch of 64 at 512 - 4096 tokens).  The step's own rows (16-bit K and V) are added by
 // plain 32-bit arithmetic.  Warps, then the CTAs of a sequence cut into chunks,
 // merge their (m, l, O); of the latter the one that arrives last, in chunk order,
 // so that results do not depend on the order of arrival.
@@ -56,18 +58,11 @@ struct Smem {
   static constexpr int kscale = page + 4 * kGroups;                  // float [kGroups]: 2^e of K, NaN: no such page
   static constexpr int vexp = kscale + 4 * kGroups;                  // float [kGroups]: e of V
   static constexpr int anc = vexp + 4 * kGroups;                     // uint64 [16 rows][2]
-  static constexpr int misc = anc + 16 * 16;
+  static constexpr int bars = anc + 16 * 16;                          // uint64 [kWarps][kStages]
+  static constexpr int misc = bars + 8 * kWarps * kStages;
   static constexpr int end = misc + 16;
+  static constexpr int dyn = end + 1024;                              // to a 1024-byte boundary (the swizzle's atom)
 };
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 // two e4m3 codes (low byte first) as two fp16: exact
 __device__ __forceinline__ uint32_t cvt_e4m3x2(uint32_t w16) {
@@ -113,8 +108,10 @@ __device__ __forceinline__ void load16(const T* p, float (&v)[16]) {
 }
 
 template <typename T, int NT>
-__global__ void __launch_bounds__(kThreads) kv8_decode_kernel(Kv8View c, spec_kv8_attention_args a, DecodePlan pl) {
-  extern __shared__ __align__(16) uint8_t smem[];
+__global__ void __launch_bounds__(kThreads) kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8View c,
+                                                              spec_kv8_attention_args a, DecodePlan pl) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   int* s_page = reinterpret_cast<int*>(smem + Smem::page);
   float* s_kscale = reinterpret_cast<float*>(smem + Smem::kscale);
   float* s_vexp = reinterpret_cast<float*>(smem + Smem::vexp);
@@ -139,6 +136,9 @@ __global__ void __launch_bounds__(kThreads) kv8_decode_kernel(Kv8View c, spec_kv
   const int ngroups = (c1 - c0 + 15) >> 4;
   const int ntiles = (c1 - c0 + kTile - 1) / kTile;
 
+  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + Smem::bars) + warp * kStages;
+  if (lane < kStages) mbar_init(&full[lane], 1);
+  fence_barrier_init();
   // pages of the chunk's groups of 16 keys
   for (int i = tid; i < 2 * ntiles; i += kThreads) {
     const int key = c0 + 16 * i;
@@ -188,10 +188,10 @@ __global__ void __launch_bounds__(kThreads) kv8_decode_kernel(Kv8View c, spec_kv
     const int rr = min(r, rows - 1);
     const int node = rr / G;
     const T* p = reinterpret_cast<const T*>(a.q) + a.q_row_stride * (first + node) +
-                 a.q_head_stride * (kvh * G + (rr - node * G)) + 16 * t;
+                 a.q_head_stride * (kvh * G + (rr - node * G)) + 32 * t;
     float v[32];
     load16(p, reinterpret_cast<float(&)[16]>(v[0]));
-    load16(p + 64, reinterpret_cast<float(&)[16]>(v[16]));
+    load16(p + 16, reinterpret_cast<float(&)[16]>(v[16]));
     int ex = 0;
     if (sizeof(T) == 2 && !__is_same(T, __half)) {
       float m = 0.f;
@@ -218,28 +218,24 @@ __global__ void __launch_bounds__(kThreads) kv8_decode_kernel(Kv8View c, spec_kv
   }
   __syncthreads();
 
-  const uint32_t ring = smem_u32(smem + Smem::ring) + warp * (kStages * kTileBytes) + lane * 16;
+  uint8_t* const ring = smem + Smem::ring + warp * (kStages * kTileBytes);
   const int mine = ntiles > warp ? (ntiles - warp + kWarps - 1) / kWarps : 0;
+  // tile i of this warp: K of two groups of 16 keys, then V
   auto fetch = [&](int i) {
-    if (i < mine) {
-      const uint32_t dst = ring + (i % kStages) * kTileBytes;
-      const int g0 = 2 * (warp + kWarps * i);
+    if (lane == 0 && i < mine) {
+      const int st = i % kStages, g0 = 2 * (warp + kWarps * i);
+      const uint64_t pol = policy_evict_first();
+      mbar_arrive_expect_tx(&full[st], kTileBytes);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const size_t base = (size_t)s_page[g0 + u] * (16 * kKv8Hd);
-        const uint8_t* k = c.codes[0] + base + g * kKv8Hd + 16 * t;
-        const uint8_t* v = c.codes[1] + base + 2 * t * kKv8Hd + 16 * g;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          cp_async16(dst + (8 * u + j) * 512, k + (j >> 1) * 8 * kKv8Hd + (j & 1) * 64);
-          cp_async16(dst + (8 * u + 4 + j) * 512, v + ((j >> 1) * 8 + (j & 1)) * kKv8Hd);
-        }
-      }
+      for (int q = 0; q < 4; ++q)
+        tma_load_2d(ring + st * kTileBytes + q * 2048, &map, &full[st], 0, c.row0[q >> 1] + 16 * s_page[g0 + (q & 1)], pol);
     }
-    cp_async_commit();
   };
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) fetch(i);
+  for (int i = 0; i < kStages; ++i) fetch(i);
+  // where lane (g, t) finds its pieces: row g of K, pieces 2t and 2t + 1; rows 2t, 2t + 1, + 8, + 9 of V, piece g
+  const int k_at0 = g * 128 + (((2 * t) ^ g) << 4), k_at1 = g * 128 + (((2 * t + 1) ^ g) << 4);
+  const int v_at0 = 2 * t * 128 + ((g ^ (2 * t)) << 4), v_at1 = (2 * t + 1) * 128 + ((g ^ (2 * t + 1)) << 4);
 
   float m[NT][2], l[NT][2], o[NT][8][4];
 #pragma unroll
@@ -263,17 +259,18 @@ __global__ void __launch_bounds__(kThreads) kv8_decode_kernel(Kv8View c, spec_kv
     }
   };
 
+  bool landed = true;
   for (int i = 0; i < mine; ++i) {
-    fetch(i + kStages - 1);
-    cp_async_wait<kStages - 1>();
-    const uint4* buf = reinterpret_cast<const uint4*>(smem + Smem::ring + warp * (kStages * kTileBytes) +
-                                                      (i % kStages) * kTileBytes) + lane;
+    landed = mbar_wait(&full[i % kStages], (i / kStages) & 1, nullptr, nullptr) && landed;
+    landed = __all_sync(0xffffffffu, landed);
+    const uint8_t* const buf = ring + (i % kStages) * kTileBytes;
+    auto piece = [&](int at) { return *reinterpret_cast<const uint4*>(buf + at); };
     const int g0 = 2 * (warp + kWarps * i);
     float s[2][NT][4];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const uint4 ka0 = buf[(8 * u + 0) * 32], ka1 = buf[(8 * u + 1) * 32];  // key g
-      const uint4 kb0 = buf[(8 * u + 2) * 32], kb1 = buf[(8 * u + 3) * 32];  // key g + 8
+      const uint4 ka0 = piece(2048 * u + k_at0), ka1 = piece(2048 * u + k_at1);                // key g
+      const uint4 kb0 = piece(2048 * u + 1024 + k_at0), kb1 = piece(2048 * u + 1024 + k_at1);  // key g + 8
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) s[u][nt][0] = s[u][nt][1] = s[u][nt][2] = s[u][nt][3] = 0.f;
 #pragma unroll
@@ -329,7 +326,8 @@ __global__ void __launch_bounds__(kThreads) kv8_decode_kernel(Kv8View c, spec_kv
     }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      uint4 v0 = buf[(8 * u + 4) * 32], v1 = buf[(8 * u + 5) * 32], v2 = buf[(8 * u + 6) * 32], v3 = buf[(8 * u + 7) * 32];
+      uint4 v0 = piece(4096 + 2048 * u + v_at0), v1 = piece(4096 + 2048 * u + v_at1);
+      uint4 v2 = piece(5120 + 2048 * u + v_at0), v3 = piece(5120 + 2048 * u + v_at1);
       if (left < 16 * u + 16) {  // what lies behind the sequence's end may be anything: 0 * NaN would spread
         const int k0 = left - 16 * u - 2 * t;
         if (k0 <= 0) v0 = make_uint4(0, 0, 0, 0);
@@ -351,19 +349,24 @@ __global__ void __launch_bounds__(kThreads) kv8_decode_kernel(Kv8View c, spec_kv
         }
       }
     }
+    __syncwarp();  // every lane has used what it read: the stage may be filled again
+    fetch(i + kStages);
   }
-  cp_async_wait<0>();
+  if (!landed) {  // a wait ran out: the rows say so
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) l[nt][0] = l[nt][1] = NAN;
+  }
 
   // the step's own rows: the last chunk's CTA, its warps in turn
   if (a.k_new && chunk_i == nc - 1) {
     // rows of the tile see no row behind the tile's last node
     const int top = min(n - 1, (row0 + kRows - 1) / G);
     for (int j = warp; j <= top; j += kWarps) {
-      const T* kp = reinterpret_cast<const T*>(a.k_new) + a.k_row_stride * (first + j) + a.k_head_stride * kvh + 16 * t;
+      const T* kp = reinterpret_cast<const T*>(a.k_new) + a.k_row_stride * (first + j) + a.k_head_stride * kvh + 32 * t;
       const T* vp = reinterpret_cast<const T*>(a.v_new) + a.v_row_stride * (first + j) + a.v_head_stride * kvh + 16 * g;
       float k[32], v[16];
       load16(kp, reinterpret_cast<float(&)[16]>(k[0]));
-      load16(kp + 64, reinterpret_cast<float(&)[16]>(k[16]));
+      load16(kp + 16, reinterpret_cast<float(&)[16]>(k[16]));
       load16(vp, v);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -522,11 +525,12 @@ cudaError_t kv8_attention_configure() {
   cudaError_t e = kv8_tree_configure();
   for (const void* f : {(const void*)kv8_decode_kernel<__nv_bfloat16, 1>, (const void*)kv8_decode_kernel<__nv_bfloat16, 2>,
                         (const void*)kv8_decode_kernel<__half, 1>, (const void*)kv8_decode_kernel<__half, 2>})
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::end);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::dyn);
   return e;
 }
 
-cudaError_t launch_kv8_attention(const Kv8View& c, const spec_kv8_attention_args& a, int sm_count, cudaStream_t s) {
+cudaError_t launch_kv8_attention(const Kv8View& c, const CUtensorMap& map, const spec_kv8_attention_args& a, int sm_count,
+                                 cudaStream_t s) {
   if (by_tree(c.hkv, a.n_q_heads, a.max_nodes, a.max_prefix)) return launch_kv8_tree(c, a, sm_count, s);
   int nt = 1;
   size_t bytes = 0;
@@ -538,11 +542,11 @@ cudaError_t launch_kv8_attention(const Kv8View& c, const spec_kv8_attention_args
   p.part = reinterpret_cast<float*>(p.ml + groups * p.chunks * 8 * nt);
   const unsigned grid = (unsigned)(groups * p.chunks);
   if (a.dtype == SPEC_DTYPE_BF16) {
-    if (nt == 1) kv8_decode_kernel<__nv_bfloat16, 1><<<grid, kThreads, Smem::end, s>>>(c, a, p);
-    else kv8_decode_kernel<__nv_bfloat16, 2><<<grid, kThreads, Smem::end, s>>>(c, a, p);
+    if (nt == 1) kv8_decode_kernel<__nv_bfloat16, 1><<<grid, kThreads, Smem::dyn, s>>>(map, c, a, p);
+    else kv8_decode_kernel<__nv_bfloat16, 2><<<grid, kThreads, Smem::dyn, s>>>(map, c, a, p);
   } else {
-    if (nt == 1) kv8_decode_kernel<__half, 1><<<grid, kThreads, Smem::end, s>>>(c, a, p);
-    else kv8_decode_kernel<__half, 2><<<grid, kThreads, Smem::end, s>>>(c, a, p);
+    if (nt == 1) kv8_decode_kernel<__half, 1><<<grid, kThreads, Smem::dyn, s>>>(map, c, a, p);
+    else kv8_decode_kernel<__half, 2><<<grid, kThreads, Smem::dyn, s>>>(map, c, a, p);
   }
   return cudaGetLastError();
 }
