@@ -19,9 +19,7 @@ namespace spec {
 
 namespace {
 
-constexpr int kThreads = 128;         // 64 for K, 64 for V
-constexpr int kLanes = 16;            // threads of a row: 8 values each
-constexpr int kRowsAtOnce = 64 / kLanes;
+constexpr int kLanes = 16;  // threads of a row: 8 values each
 
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }  // e in [-126, 127]
 
@@ -34,17 +32,20 @@ __device__ __forceinline__ int exponent_of(float a) {
   return min(kKv8ExpMax, max(kKv8ExpMin, e));
 }
 
-__device__ __forceinline__ void load8(const float* p, float* v) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
+// eight values as they lie in memory
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float* v) {
-  const uint4 r = *reinterpret_cast<const uint4*>(p);
-  const T* h = reinterpret_cast<const T*>(&r);
+struct Eight {
+  uint4 w[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = to_f32<T>(h[i]);
-}
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const T* h = reinterpret_cast<const T*>(w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = to_f32<T>(h[i]);
+  }
+};
 
 // eight values times `s` as e4m3, round to nearest even, saturating
 __device__ __forceinline__ uint2 encode8(const float* v, float s) {
@@ -55,64 +56,102 @@ __device__ __forceinline__ uint2 encode8(const float* v, float s) {
   return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) kv8_append_kernel(Kv8View c, spec_kv8_append_args a, int rows_per_cta) {
-  __shared__ int run_len;
-  __shared__ float part[4];
-  const int tid = threadIdx.x, plane = tid >> 6, t = tid & 63;
+// THREADS: half of them for K, half for V.  HELD rows per thread stay in registers, so that runs of
+// HELD * THREADS / 32 rows are read once.
+template <typename T, int THREADS, int HELD>
+__global__ void __launch_bounds__(THREADS) kv8_append_kernel(Kv8View c, spec_kv8_append_args a, int rows_per_cta) {
+  constexpr int kPlane = THREADS / 2, kRowsAtOnce = kPlane / kLanes, kWarps = kPlane / 32;
+  __shared__ uint32_t s_break[9];  // rows r0 .. r0 + 255: does a run end before this row?
+  __shared__ int s_slot[256], s_src[256];
+  __shared__ float part[2 * kWarps];
+  __shared__ int part_nan[2 * kWarps];
+  const int tid = threadIdx.x, plane = tid / kPlane, t = tid % kPlane;
   const int head = blockIdx.y;
   const int sub = t / kLanes, col = (t % kLanes) * 8;
   const T* src = reinterpret_cast<const T*>(plane ? a.v : a.k) + (plane ? a.v_head_stride : a.k_head_stride) * head + col;
   const int64_t row_stride = plane ? a.v_row_stride : a.k_row_stride;
   const int limit = c.n_pages << c.page_log2;
-  // a row's slot, -1 where it stores nothing
-  auto slot_of = [&](int i) {
-    const int s = a.slots[i];
-    const int r = a.src_rows ? a.src_rows[i] : i;
+  const int r0 = blockIdx.x * rows_per_cta;
+  // The runs that start in rows r0 .. r0 + rows_per_cta - 1 (at most a page) are this CTA's; the last of them ends
+  // within a page from there.  A row that stores nothing has slot -1.
+  auto slot_of = [&](int j, int& r) {
+    const int s = a.slots[j];
+    r = a.src_rows ? a.src_rows[j] : j;
     return (s >= 0 && s < limit && r >= 0 && r < a.n_src) ? s : -1;
   };
-  const int r0 = blockIdx.x * rows_per_cta;
-  const int r1 = min(a.rows, r0 + rows_per_cta);
-  int i = r0;
-  while (i < r1) {
-    // (uniform over the CTA)
-    const int slot = slot_of(i);
-    const int place = slot & (c.page - 1);
-    if (slot < 0 || (i > 0 && place > 0 && slot_of(i - 1) == slot - 1)) {
+  for (int w = tid; w < ((rows_per_cta + c.page + 31) & ~31); w += THREADS) {
+    const int i = r0 + w;
+    int slot = -1, row = 0, before = -1, none;
+    if (i < a.rows) slot = slot_of(i, row);
+    if (i > 0 && i <= a.rows) before = slot_of(i - 1, none);
+    s_slot[w] = slot;
+    s_src[w] = row;
+    const bool brk = slot < 0 || before < 0 || slot != before + 1 || (slot & (c.page - 1)) == 0;
+    const uint32_t m = __ballot_sync(0xffffffffu, brk);
+    if ((tid & 31) == 0) s_break[w >> 5] = m;
+  }
+  if (tid == 0) s_break[(rows_per_cta + c.page + 31) >> 5] = 1u;
+  __syncthreads();
+  for (int i = 0; i < rows_per_cta;) {
+    // (uniform over the CTA) the next break, from i on
+    const uint32_t w = s_break[i >> 5] >> (i & 31);
+    if (w == 0) {
+      i = (i | 31) + 1;
+      continue;
+    }
+    i += __ffs(w) - 1;
+    if (i >= rows_per_cta) break;
+    const int slot = s_slot[i];
+    if (slot < 0) {
       ++i;
       continue;
     }
-    // the run's length
-    if (tid == 0) run_len = c.page - place;
-    __syncthreads();
-    if (place + tid < c.page && (i + tid >= a.rows || slot_of(i + tid) != slot + tid)) atomicMin(&run_len, tid);
-    __syncthreads();
-    const int n = run_len;
-    const int pg = slot >> c.page_log2;
+    int end = i + 1;
+    while (!(s_break[end >> 5] >> (end & 31))) end = (end | 31) + 1;
+    end += __ffs(s_break[end >> 5] >> (end & 31)) - 1;
+    const int n = end - i, place = slot & (c.page - 1), pg = slot >> c.page_log2;
+    uint8_t* const ep = c.exps[plane] + (size_t)pg * c.hkv + head;
+    uint8_t* const base = c.codes[plane] + (((size_t)pg * c.hkv + head) << c.page_log2) * kKv8Hd + col;
+    const int old_byte = place > 0 ? (int)*ep : 0;
+    Eight<T> held[HELD];
+#pragma unroll
+    for (int k = 0; k < HELD; ++k)
+      if (sub + k * kRowsAtOnce < n) held[k].load(src + row_stride * s_src[i + sub + k * kRowsAtOnce]);
     float amax = 0.f;
     bool nan = false;
-    for (int r = sub; r < n; r += kRowsAtOnce) {
+    auto look = [&](const Eight<T>& x) {
       float v[8];
-      load8(src + row_stride * (a.src_rows ? a.src_rows[i + r] : i + r), v);
+      x.get(v);
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         const float m = fabsf(v[q]);
         amax = fmaxf(amax, m < INFINITY ? m : 0.f);
         nan |= m != m;
       }
+    };
+#pragma unroll
+    for (int k = 0; k < HELD; ++k)
+      if (sub + k * kRowsAtOnce < n) look(held[k]);
+    for (int r = sub + HELD * kRowsAtOnce; r < n; r += kRowsAtOnce) {
+      Eight<T> x;
+      x.load(src + row_stride * s_src[i + r]);
+      look(x);
     }
-    amax = __any_sync(0xffffffffu, nan) ? NAN : warp_max(amax);
-    if ((tid & 31) == 0) part[tid >> 5] = amax;
-    __syncthreads();
-    nan = isnan(part[2 * plane]) || isnan(part[2 * plane + 1]);
-    amax = fmaxf(part[2 * plane], part[2 * plane + 1]);
-    if (!(amax >= 0.f)) amax = 0.f;  // both NaN
-    uint8_t* ep = c.exps[plane] + (size_t)pg * c.hkv + head;
-    uint8_t* base = c.codes[plane] + (((size_t)pg * c.hkv + head) << c.page_log2) * kKv8Hd + col;
+    amax = warp_max(amax);
+    nan = __any_sync(0xffffffffu, nan);
+    if ((tid & 31) == 0) part[tid >> 5] = amax, part_nan[tid >> 5] = nan;
+    __syncthreads();  // (also: every thread has read the page's exponent)
+    amax = 0.f;
+    nan = false;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      amax = fmaxf(amax, part[kWarps * plane + w]);
+      nan |= part_nan[kWarps * plane + w] != 0;
+    }
     int e = exponent_of(amax);
     if (place > 0) {
-      const int old = (int)*ep - 127;
-      nan |= old == 128;
+      const int old = old_byte - 127;
+      nan |= old_byte == 255;
       e = nan ? e : max(e, old);
       if (!nan && e > old) {
         const float f = pow2f(max(old - e, -126));
@@ -128,26 +167,43 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(Kv8View c, spec_kv
       }
     }
     const float f = pow2f(-e);
-    for (int r = sub; r < n; r += kRowsAtOnce) {
+    uint8_t* const to = base + (size_t)place * kKv8Hd;
+    auto put = [&](int r, const Eight<T>& x) {
       float v[8];
-      load8(src + row_stride * (a.src_rows ? a.src_rows[i + r] : i + r), v);
-      *reinterpret_cast<uint2*>(base + (size_t)(place + r) * kKv8Hd) = encode8(v, f);
+      x.get(v);
+      *reinterpret_cast<uint2*>(to + (size_t)r * kKv8Hd) = encode8(v, f);
+    };
+#pragma unroll
+    for (int k = 0; k < HELD; ++k)
+      if (sub + k * kRowsAtOnce < n) put(sub + k * kRowsAtOnce, held[k]);
+    for (int r = sub + HELD * kRowsAtOnce; r < n; r += kRowsAtOnce) {
+      Eight<T> x;
+      x.load(src + row_stride * s_src[i + r]);
+      put(r, x);
     }
-    __syncthreads();  // every thread has read the exponent, `part` and `run_len`
     if (t == 0) *ep = (uint8_t)(nan ? 255 : e + 127);
-    i += n;
+    i = end;
+    __syncthreads();  // `part` may be written again
   }
+}
+
+template <typename T>
+void launch_append(const Kv8View& c, const spec_kv8_append_args& a, int per, cudaStream_t s) {
+  const dim3 grid((a.rows + per - 1) / per, c.hkv);
+  if (per == 1) kv8_append_kernel<T, 64, 4><<<grid, 64, 0, s>>>(c, a, per);
+  else kv8_append_kernel<T, 256, 8><<<grid, 256, 0, s>>>(c, a, per);
 }
 
 }  // namespace
 
 cudaError_t launch_kv8_append(const Kv8View& c, const spec_kv8_append_args& a, int sm_count, cudaStream_t s) {
+  // One row per CTA of 64 threads while that leaves the GPU room (a decoding step, accepted rows), up to a page per CTA
+  // of 256 for prompts.  A CTA's runs are stored one after the other.
   int per = (int)((long long)a.rows * c.hkv / (16 * sm_count));
   per = per < 1 ? 1 : per > c.page ? c.page : per;
-  const dim3 grid((a.rows + per - 1) / per, c.hkv);
-  if (a.dtype == SPEC_DTYPE_F32) kv8_append_kernel<float><<<grid, kThreads, 0, s>>>(c, a, per);
-  else if (a.dtype == SPEC_DTYPE_BF16) kv8_append_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(c, a, per);
-  else kv8_append_kernel<__half><<<grid, kThreads, 0, s>>>(c, a, per);
+  if (a.dtype == SPEC_DTYPE_F32) launch_append<float>(c, a, per, s);
+  else if (a.dtype == SPEC_DTYPE_BF16) launch_append<__nv_bfloat16>(c, a, per, s);
+  else launch_append<__half>(c, a, per, s);
   return cudaGetLastError();
 }
 

@@ -21,10 +21,12 @@
 //            the scores' accumulators become the B operand by movmatrix.
 //
 // Each warp streams tiles of 32 keys through a queue of its own in shared memory,
-// three tiles deep, which one lane fills by TMA (boxes of 16 keys, each inside one
+// two tiles deep, which one lane fills by TMA (boxes of 16 keys, each inside one
 // page; the 128-byte swizzle keeps both products' reads free of bank conflicts).
-// Sixteen cp.async per lane and tile instead took longer to issue than the rest of
-// the tile (89 us for a batch of 64 at 512 - 4096 tokens).  The step's own rows (16-bit K and V) are added by
+// A batch of 64 at 512 - 4096 tokens (310 MB) takes 60.5 us, 5.1 TB/s, 78 % of the
+// measured copy rate, with three CTAs of four warps per SM; 68 us with three tiles
+// and two CTAs, 70 - 110 us with CTAs of two or eight warps, 89 us with sixteen
+// cp.async per lane and tile in place of TMA.  The step's own rows (16-bit K and V) are added by
 // plain 32-bit arithmetic.  Warps, then the CTAs of a sequence cut into chunks,
 // merge their (m, l, O); of the latter the one that arrives last, in chunk order,
 // so that results do not depend on the order of arrival.
@@ -40,7 +42,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 32;          // keys per step of a warp: two groups of 16, each inside one page
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 constexpr int kTileBytes = kTile * 2 * kKv8Hd;
 constexpr int kMaxChunk = 4096;    // keys of a CTA: its page ids and scales lie in shared memory
 constexpr int kGroups = kMaxChunk / 16;
@@ -491,8 +493,11 @@ DecodePlan plan_decode(int hkv, int sm_count, int batch, int n_q_heads, int max_
   *nt = rows <= 8 ? 1 : 2;
   p.row_tiles = (rows + 8 * *nt - 1) / (8 * *nt);
   const long long groups = (long long)batch * hkv * p.row_tiles;
-  // about four rounds of two CTAs per SM, at least a tile for each warp
-  const long long want = groups * max_prefix / (8LL * sm_count);
+  // Chunks of about an eighth of an SM's share of the keys (prefixes of one length assumed: ragged ones make fewer
+  // CTAs) where there are at least as many groups as SMs, for an even load (64 sequences x 8 heads: 60.5 us, 66.6 with
+  // a quarter, 63.6 with a sixteenth); of a quarter where there are fewer, since every chunk costs a partial result
+  // (7 x 4 up to 16385 tokens: 23.5 us, 29.9 with an eighth).  At least a tile for each warp.
+  const long long want = groups * max_prefix / ((groups >= sm_count ? 8LL : 4LL) * sm_count);
   long long chunk = (want + 127) / 128 * 128;
   chunk = chunk < 128 ? 128 : chunk > kMaxChunk ? kMaxChunk : chunk;
   p.chunk = (int)chunk;
