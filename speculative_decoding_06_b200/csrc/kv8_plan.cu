@@ -32,13 +32,14 @@ struct PlanSmem {
   int* need;  // [batch] pages taken before each entry
   int* back;  // [batch + 1] pages given back before each entry
   int* cur;   // [batch] length before the step
+  int* id;    // [batch] sequence
 };
 
 __device__ __forceinline__ int blocks_of(int n, int lg) { return (int)(((unsigned)n + (1u << lg) - 1u) >> lg); }
 
-// inclusive sums over the block of three values; `part` holds one triple per warp
-__device__ __forceinline__ void block_scan3(long long v[3], long long (*part)[3], long long carry[3]) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n_warps = blockDim.x >> 5;
+// Inclusive sums over the block of three values, on top of `carry`, which becomes the block's total; `part` holds one
+// triple per warp and one more.
+__device__ __forceinline__ void warp_scan3(long long v[3], int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
 #pragma unroll
@@ -47,23 +48,32 @@ __device__ __forceinline__ void block_scan3(long long v[3], long long (*part)[3]
       if (lane >= o) v[q] += u;
     }
   }
+}
+__device__ __forceinline__ void block_scan3(long long v[3], long long (*part)[3], long long carry[3]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n_warps = blockDim.x >> 5;
+  warp_scan3(v, lane);
   if (lane == 31) {
 #pragma unroll
     for (int q = 0; q < 3; ++q) part[warp][q] = v[q];
   }
   __syncthreads();
-  long long total[3] = {carry[0], carry[1], carry[2]};
-  for (int w = 0; w < n_warps; ++w) {
+  if (warp == 0) {
+    long long w[3] = {0, 0, 0};
+    if (lane < n_warps) {
 #pragma unroll
-    for (int q = 0; q < 3; ++q) {
-      if (w < warp) v[q] += part[w][q];
-      total[q] += part[w][q];
+      for (int q = 0; q < 3; ++q) w[q] = part[lane][q];
+    }
+    warp_scan3(w, lane);
+    if (lane < n_warps) {
+#pragma unroll
+      for (int q = 0; q < 3; ++q) part[lane][q] = w[q];
     }
   }
+  __syncthreads();
 #pragma unroll
   for (int q = 0; q < 3; ++q) {
-    v[q] += carry[q];
-    carry[q] = total[q];
+    v[q] += carry[q] + (warp ? part[warp - 1][q] : 0);
+    carry[q] += part[n_warps - 1][q];
   }
   __syncthreads();
 }
@@ -89,7 +99,7 @@ __device__ void fill_slots(const spec_kv8_plan_args& a, const PlanSmem& sm, int 
       const int pos = sm.cur[b] + (i - sm.off[b]);
       const int block = pos >> lg;
       const int k = block - blocks_of(sm.cur[b], lg);
-      int* entry = a.tables + (size_t)(a.seq_ids ? a.seq_ids[b] : b) * a.max_blocks + block;
+      int* entry = a.tables + (size_t)sm.id[b] * a.max_blocks + block;
       const int place = pos & ((1 << lg) - 1);
       int pg;
       if (k >= 0) {
@@ -109,27 +119,31 @@ __device__ void fill_slots(const spec_kv8_plan_args& a, const PlanSmem& sm, int 
 __global__ void __launch_bounds__(kPlanThreads) kv8_plan_kernel(spec_kv8_plan_args a, int lg, int n_pages) {
   extern __shared__ int sm_raw[];
   __shared__ long long part[kPlanThreads / 32][3];
+  __shared__ int s_bad;
   const int n = a.batch, tid = threadIdx.x;
   PlanSmem sm;
   sm.off = sm_raw;
   sm.back = sm.off + n + 1;
   sm.need = sm.back + n + 1;
   sm.cur = sm.need + n;
-  unsigned* seen = reinterpret_cast<unsigned*>(sm.cur + n);
+  sm.id = sm.cur + n;
+  unsigned* seen = reinterpret_cast<unsigned*>(sm.id + n);
   const int words = a.seq_ids ? (a.n_seqs + 31) >> 5 : 0;
-  for (int i = tid; i < words; i += kPlanThreads) seen[i] = 0u;
+  const int threads = blockDim.x;
+  for (int i = tid; i < words; i += threads) seen[i] = 0u;
+  if (tid == 0) s_bad = 0;
   const int head = a.state[0], count = a.state[1];
   __syncthreads();
   int bad = 0;
   if (head < 0 || head >= n_pages || count < 0 || count > n_pages) bad |= SPEC_KV8_INDEX;
   const long long cap = (long long)a.max_blocks << lg;
   long long carry[3] = {0, 0, 0};
-  for (int b0 = 0; b0 < n; b0 += kPlanThreads) {
+  for (int b0 = 0; b0 < n; b0 += threads) {
     const int b = b0 + tid;
     long long v[3] = {0, 0, 0};
-    int cur = 0;
+    int cur = 0, id = 0;
     if (b < n) {
-      const int id = a.seq_ids ? a.seq_ids[b] : b;
+      id = a.seq_ids ? a.seq_ids[b] : b;
       bool ok = id >= 0 && id < a.n_seqs;
       if (ok && a.seq_ids) ok = !(atomicOr(&seen[id >> 5], 1u << (id & 31)) >> (id & 31) & 1u);
       if (ok) {
@@ -155,33 +169,27 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_plan_kernel(spec_kv8_plan_ar
       sm.need[b] = (int)(v[1] - own[1]);
       sm.back[b] = (int)(v[2] - own[2]);
       sm.cur[b] = cur;
+      sm.id[b] = id;
     }
   }
   if (carry[0] > a.max_rows) bad |= SPEC_KV8_ROWS;
   if (carry[1] > count) bad |= SPEC_KV8_PAGES;
   if (carry[2] + count > n_pages) bad |= SPEC_KV8_INDEX;  // more pages than the pool has
-  int status = 0;
-#pragma unroll
-  for (int bit = 1; bit <= SPEC_KV8_INDEX; bit <<= 1)
-    if (__syncthreads_or(bad & bit)) status |= bit;
-  const int total = status ? 0 : (int)carry[0];
+  bad = __reduce_or_sync(0xffffffffu, bad);
+  if ((tid & 31) == 0 && bad) atomicOr(&s_bad, bad);
   if (tid == 0) {
     sm.off[n] = (int)carry[0];
     sm.back[n] = (int)carry[2];
   }
+  // (every input length is read by here: the output may be the same array)
+  if (a.lengths_out != a.lengths)
+    for (int i = tid; i < a.n_seqs; i += threads) a.lengths_out[i] = a.lengths[i];
   __syncthreads();
-  // the new lengths (every input length is read before any is written: they may be one array)
-  for (int s0 = 0; s0 < a.n_seqs; s0 += kPlanThreads) {
-    const int s = s0 + tid;
-    if (s < a.n_seqs && a.lengths_out != a.lengths) a.lengths_out[s] = a.lengths[s];
-  }
-  __syncthreads();
-  for (int b = tid; b < n; b += kPlanThreads) {
+  const int status = s_bad;
+  const int total = status ? 0 : (int)carry[0];
+  for (int b = tid; b < n; b += threads) {
     a.offsets[b] = status ? 0 : sm.off[b];
-    if (!status) {
-      const int id = a.seq_ids ? a.seq_ids[b] : b;
-      a.lengths_out[id] = (int)max(0ll, (long long)sm.cur[b] + a.add[b]);
-    }
+    if (!status) a.lengths_out[sm.id[b]] = (int)max(0ll, (long long)sm.cur[b] + a.add[b]);
   }
   if (tid == 0) {
     int h2 = head, c2 = count;
@@ -196,16 +204,16 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_plan_kernel(spec_kv8_plan_ar
   }
   if (!status) {
     const int given = sm.back[n];
-    for (int j = tid; j < given; j += kPlanThreads) {
+    for (int j = tid; j < given; j += threads) {
       const int b = entry_of(sm.back, n, j);
-      const int id = a.seq_ids ? a.seq_ids[b] : b;
-      const long long next = max(0ll, (long long)sm.cur[b] + a.add[b]);
-      const int block = blocks_of((int)next, lg) + (j - sm.back[b]);
-      a.ring[((long long)head + count + j) % n_pages] = a.tables[(size_t)id * a.max_blocks + block];
+      const int kept = blocks_of(sm.cur[b], lg) - (sm.back[b + 1] - sm.back[b]);
+      int at = head + count + j;  // < 3 n_pages
+      at -= at >= 2 * n_pages ? 2 * n_pages : at >= n_pages ? n_pages : 0;
+      a.ring[at] = a.tables[(size_t)sm.id[b] * a.max_blocks + kept + (j - sm.back[b])];
     }
   }
   if (a.max_rows <= kPlanOwnRows)
-    fill_slots(a, sm, lg, n_pages, head, total, tid, kPlanThreads);
+    fill_slots(a, sm, lg, n_pages, head, total, tid, threads);
 }
 
 // The slots of many new rows, from what kv8_plan_kernel wrote.
@@ -218,6 +226,7 @@ __global__ void __launch_bounds__(kFillThreads) kv8_fill_kernel(spec_kv8_plan_ar
   sm.back = nullptr;
   sm.need = sm.off + n + 1;
   sm.cur = sm.need + n;
+  sm.id = sm.cur + n;
   pdl_wait();
   const int total = a.offsets[n];
   long long carry[3] = {0, 0, 0};
@@ -225,11 +234,12 @@ __global__ void __launch_bounds__(kFillThreads) kv8_fill_kernel(spec_kv8_plan_ar
     for (int b0 = 0; b0 < n; b0 += kFillThreads) {
       const int b = b0 + tid;
       long long v[3] = {0, 0, 0};
-      int off = 0, cur = 0;
+      int off = 0, cur = 0, id = 0;
       if (b < n) {
         off = a.offsets[b];
         const int rows = a.offsets[b + 1] - off;
-        const int next = a.lengths_out[a.seq_ids ? a.seq_ids[b] : b];
+        id = a.seq_ids ? a.seq_ids[b] : b;
+        const int next = a.lengths_out[id];
         cur = next - rows;
         if (rows > 0) v[1] = blocks_of(next, lg) - blocks_of(cur, lg);
       }
@@ -239,6 +249,7 @@ __global__ void __launch_bounds__(kFillThreads) kv8_fill_kernel(spec_kv8_plan_ar
         sm.off[b] = off;
         sm.need[b] = (int)(v[1] - own);
         sm.cur[b] = cur;
+        sm.id[b] = id;
       }
     }
     if (tid == 0) sm.off[n] = total;
@@ -250,7 +261,7 @@ __global__ void __launch_bounds__(kFillThreads) kv8_fill_kernel(spec_kv8_plan_ar
 }
 
 size_t plan_smem(int batch, int n_seqs, bool ids) {
-  return 4 * (4 * (size_t)batch + 2) + (ids ? 4 * (size_t)((n_seqs + 31) / 32) : 0);
+  return 4 * (5 * (size_t)batch + 2) + (ids ? 4 * (size_t)((n_seqs + 31) / 32) : 0);
 }
 
 }  // namespace
@@ -260,19 +271,21 @@ cudaError_t kv8_plan_configure() {
                                        (int)plan_smem(kKv8MaxBatch, kKv8MaxSeqs, true));
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(kv8_fill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             4 * (3 * kKv8MaxBatch + 1));
+                             4 * (4 * kKv8MaxBatch + 1));
   return e;
 }
 
 cudaError_t launch_kv8_plan(const spec_kv8_plan_args& a, int page_log2, int n_pages, cudaStream_t s) {
-  kv8_plan_kernel<<<1, kPlanThreads, plan_smem(a.batch, a.n_seqs, a.seq_ids != nullptr), s>>>(a, page_log2, n_pages);
+  // a small step is bound by the latency of its barriers: fewer warps
+  const int threads = a.batch <= 32 && a.max_rows <= 1024 ? 256 : kPlanThreads;
+  kv8_plan_kernel<<<1, threads, plan_smem(a.batch, a.n_seqs, a.seq_ids != nullptr), s>>>(a, page_log2, n_pages);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || a.max_rows <= kPlanOwnRows) return e;
   cudaLaunchConfig_t cfg = {};
   const int ctas = (a.max_rows + kFillThreads - 1) / kFillThreads;
   cfg.gridDim = dim3(ctas < 592 ? ctas : 592);
   cfg.blockDim = dim3(kFillThreads);
-  cfg.dynamicSmemBytes = 4 * (3 * (size_t)a.batch + 1);
+  cfg.dynamicSmemBytes = 4 * (4 * (size_t)a.batch + 1);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
