@@ -347,6 +347,41 @@ class SpecEngine:
         self._check(S.spec_draft_len(self.h, seq, _ptr(ln)))
         return int(ln[0])
 
+    def export_kv8(self, seq_ids, cache, pages, kv8_ids=None):
+        """Store the cached K/V of sequences into an 8-bit paged cache (kv8.KV8Cache with the target's layers and kv
+        heads; a third of the dense cache's bytes), so that their places here can be reused while the prefixes stay
+        readable by KV8Cache.attention.  pages: cache.page_state(...), updated in place; engine sequence seq_ids[i]
+        extends sequence kv8_ids[i] (default: i) there.  bf16 models only.  Returns the token counts."""
+        d = self.dims
+        if d.dtype != "bf16":
+            raise ValueError("export_kv8 needs a bf16 model (its cache is fp16)")
+        kv = self.kv_view()
+        if (cache.n_layers, cache.n_kv_heads) != (d.n_layers, d.n_kv_heads):
+            raise ValueError("the 8-bit cache has %d layers of %d kv heads, the target model %d of %d" % (
+                cache.n_layers, cache.n_kv_heads, d.n_layers, d.n_kv_heads))
+        ids = [int(s) for s in seq_ids]
+        to = list(range(len(ids))) if kv8_ids is None else [int(s) for s in kv8_ids]
+        lens = [self.seq_len(s)[0] for s in ids]
+        dev = cache.device
+        i32 = dict(dtype=torch.int32, device=dev)
+        plan = cache.plan(pages.lengths, torch.tensor(lens, **i32), pages.tables, pages.ring, pages.state, sum(lens),
+                          seq_ids=torch.tensor(to, **i32),
+                          out=cache.plan_buffers(len(ids), pages.lengths.shape[0], sum(lens))._replace(
+                              lengths=pages.lengths, state=pages.state))
+        if int(plan.status):
+            raise S.SpecError(S.SPEC_ERR_CAPACITY, "no room in the 8-bit cache (status %d)" % int(plan.status))
+        # a layer's plane is [seq][head][slot][128]: rows of 128 with the heads max_seq rows apart
+        max_seq, heads = kv.shape[4], d.n_kv_heads
+        src = torch.cat([torch.arange(n, **i32) + s * heads * max_seq for s, n in zip(ids, lens)])
+        n_src = (kv.shape[2] * heads - (heads - 1)) * max_seq
+        torch.cuda.current_stream().wait_stream(self.stream)
+        for layer in range(d.n_layers):
+            k, v = (kv.as_strided((n_src, heads, d.head_dim), (d.head_dim, max_seq * d.head_dim, 1),
+                                  kv[layer, plane].storage_offset()) for plane in (0, 1))
+            cache.append(layer, k, v, plan.slots, src_rows=src)
+        self.stream.wait_stream(torch.cuda.current_stream())
+        return lens
+
     def kv_view(self) -> torch.Tensor:
         """The cache as a tensor [layer][plane][max_batch][Hkv][max_seq][hd]: planes K, V (fp32 models) or
         K, V, K_lo in fp16 (bf16 models; the key is K + K_lo)."""
