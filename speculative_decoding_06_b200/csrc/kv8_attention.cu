@@ -11,11 +11,14 @@
 //            order is free, so lane (g, t) takes dimensions 32t .. 32t + 31 of keys
 //            g and g + 8: whole 16-byte pieces, each word of codes (4 dims) one
 //            k-step's two A registers after e4m3 -> fp16 conversion (exact).
-//   softmax  in 32 bits, base 2, with a running maximum per row.  A page's K
-//            scale multiplies the scores; its V scale 2^w goes into the
-//            exponent: p' = 2^(x + w - m), m the running maximum of x + w, so
-//            that O sums p' times bare codes and l sums p' 2^-w.  p' is rounded to
-//            fp16 (2^-11 of itself) for the second product only.
+//   softmax  in 32 bits, base 2.  A page's K scale multiplies the scores; its
+//            V scale 2^w goes into the exponent: p' = 2^(x + w - m), so that O sums
+//            p' times bare codes and l sums p' 2^-w.  m is 7 below the row's running
+//            maximum of x + w and moves only when exceeded by more than 15: p' <= 2^15,
+//            and fp16, to which p' is rounded (2^-11 of itself) for the second product,
+//            has its full 11 bits down to 2^-21 of the largest p'.  O is divided by the
+//            sum of the rounded p', so that a key's rounding cancels as far as its weight
+//            dominates; the log-sum-exp is that of the unrounded ones.
 //   output   O^T = V^T P^T: lane (g, t) holds dimensions 16g .. 16g+15 of keys 2t,
 //            2t+1, 2t+8, 2t+9; two keys' bytes interleave into A registers;
 //            the scores' accumulators become the B operand by movmatrix.
@@ -239,11 +242,11 @@ __global__ void __launch_bounds__(kThreads) kv8_decode_kernel(const __grid_const
   const int k_at0 = g * 128 + (((2 * t) ^ g) << 4), k_at1 = g * 128 + (((2 * t + 1) ^ g) << 4);
   const int v_at0 = 2 * t * 128 + ((g ^ (2 * t)) << 4), v_at1 = (2 * t + 1) * 128 + ((g ^ (2 * t + 1)) << 4);
 
-  float m[NT][2], l[NT][2], o[NT][8][4];
+  float m[NT][2], l[NT][2], lr[NT][2], o[NT][8][4];  // lr: the sum of the rounded probabilities
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     m[nt][0] = m[nt][1] = -INFINITY;
-    l[nt][0] = l[nt][1] = 0.f;
+    l[nt][0] = l[nt][1] = lr[nt][0] = lr[nt][1] = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -254,6 +257,7 @@ __global__ void __launch_bounds__(kThreads) kv8_decode_kernel(const __grid_const
     const float keep = m2 > m[nt][col] ? fast_exp2(m[nt][col] - m2) : 1.f;
     m[nt][col] = fmaxf(m[nt][col], m2);
     l[nt][col] *= keep;
+    lr[nt][col] *= keep;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       o[nt][i][col] *= keep;
@@ -307,11 +311,11 @@ __global__ void __launch_bounds__(kThreads) kv8_decode_kernel(const __grid_const
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
         mx[col] = v;
-        up |= v > m[nt][col];
+        up |= v > m[nt][col] + 15.f;
       }
       if (__any_sync(0xffffffffu, up)) {
-        raise(nt, 0, mx[0]);
-        raise(nt, 1, mx[1]);
+        raise(nt, 0, mx[0] - 7.f);
+        raise(nt, 1, mx[1] - 7.f);
       }
       const float n0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], n1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
 #pragma unroll
@@ -322,6 +326,10 @@ __global__ void __launch_bounds__(kThreads) kv8_decode_kernel(const __grid_const
         l[nt][0] = fmaf(p0 + p2, un, l[nt][0]);
         l[nt][1] = fmaf(p1 + p3, un, l[nt][1]);
         const __half2 lo = __floats2half2_rn(p0, p1), hi = __floats2half2_rn(p2, p3);
+        // (below 2^-14 the rounding loses bits that 2^-w may make matter, and the weight in O is small)
+        auto kept = [](float p, float rounded) { return p < 0x1p-14f ? p : rounded; };
+        lr[nt][0] = fmaf(kept(p0, __low2float(lo)) + kept(p2, __low2float(hi)), un, lr[nt][0]);
+        lr[nt][1] = fmaf(kept(p1, __high2float(lo)) + kept(p3, __high2float(hi)), un, lr[nt][1]);
         pb[u][nt][0] = transpose8x8(*reinterpret_cast<const uint32_t*>(&lo));
         pb[u][nt][1] = transpose8x8(*reinterpret_cast<const uint32_t*>(&hi));
       }
@@ -389,9 +397,9 @@ __global__ void __launch_bounds__(kThreads) kv8_decode_kernel(const __grid_const
           const float xc = __shfl_sync(0xffffffffu, x, 8 * t + 4 * col);
           const bool see = __shfl_sync(0xffffffffu, (int)sees, 8 * t + 4 * col);
           if (!see) continue;
-          raise(nt, col, xc);
+          if (xc > m[nt][col] + 15.f) raise(nt, col, xc - 7.f);
           const float p = fast_exp2(xc - (m[nt][col] == -INFINITY ? 0.f : m[nt][col]));
-          if (g == 0) l[nt][col] += p;
+          if (g == 0) l[nt][col] += p, lr[nt][col] += p;  // (nothing is rounded here)
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             o[nt][i][col] = fmaf(p, v[2 * i], o[nt][i][col]);
@@ -410,6 +418,16 @@ __global__ void __launch_bounds__(kThreads) kv8_decode_kernel(const __grid_const
       l[nt][col] += __shfl_xor_sync(0xffffffffu, l[nt][col], 4);
       l[nt][col] += __shfl_xor_sync(0xffffffffu, l[nt][col], 8);
       l[nt][col] += __shfl_xor_sync(0xffffffffu, l[nt][col], 16);
+      lr[nt][col] += __shfl_xor_sync(0xffffffffu, lr[nt][col], 4);
+      lr[nt][col] += __shfl_xor_sync(0xffffffffu, lr[nt][col], 8);
+      lr[nt][col] += __shfl_xor_sync(0xffffffffu, lr[nt][col], 16);
+      // from here on O is of the unrounded sum's size
+      const float f = lr[nt][col] == 0.f ? 1.f : l[nt][col] / lr[nt][col];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        o[nt][i][col] *= f;
+        o[nt][i][2 + col] *= f;
+      }
     }
   __syncthreads();
   float* s_o = reinterpret_cast<float*>(smem + Smem::ring);             // [warp][rows][132]

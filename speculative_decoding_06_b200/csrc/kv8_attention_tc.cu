@@ -29,9 +29,12 @@
 // Scales: the unit's K exponent (the largest of its pages'; codes of a page with a
 // smaller one are multiplied by the difference as they are converted, exact to
 // 2^-33 of the unit's largest value) multiplies the scores; its V exponent w goes
-// into the exponential: p' = 2^(x + w - m) with m a running maximum of x + w that
-// moves only when exceeded by more than 8, O sums p' times bare codes and the
-// denominator p' 2^-w.  p' is rounded to fp16 (2^-11 of itself) for the product only.
+// into the exponential: p' = 2^(x + w - m) with m 7 below a running maximum of x + w,
+// moved only when exceeded by more than 15 (p' <= 2^15, and fp16 has its full 11 bits
+// down to 2^-21 of the largest p'), O sums p' times bare codes and the denominator
+// p' 2^-w.  p' is rounded to fp16 (2^-11 of itself) for the product; O is divided by the
+// sum of the rounded p', so that a key's rounding cancels as far as its weight dominates, and
+// the log-sum-exp is that of the unrounded ones.
 //
 // The CTAs of a cluster share a sequence's prefix evenly and merge their normalised
 // outputs and log-sum-exps through distributed shared memory.
@@ -594,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
     const float qs = s_row[r];
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256 * t;  // this warp's lanes, the stream's columns
     const int n_own = (nu - t + 1) >> 1;  // the stream's units
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, l = 0.f, lr = 0.f;  // lr: of the rounded probabilities
     bool ok = true;
 #pragma unroll 1
     for (int i = 0; i < n_own; ++i) {
@@ -643,11 +646,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
           mx = fmax3(mx, fmax3(m0, __uint_as_float(s[30]), __uint_as_float(s[31])), m1);
         }
         mx = fmaf(mx, f, ve);
-        const bool up = mx > m + 8.f;
+        const float unit_max = mx;
+        const bool up = mx > m + 15.f;
         if (__any_sync(0xffffffffu, up)) {
+          mx -= 7.f;
           const float keep = up ? fast_exp2(m - mx) : 1.f;
           m = up ? mx : m;
           l *= keep;
+          lr *= keep;
           if (i > 0) {
             // O shrinks: the product of the stream's last unit has to be in it
             ok = __all_sync(0xffffffffu, held(B_PV + (sb ^ 1), ((i - 1) >> 1) & 1));
@@ -678,15 +684,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
             f2_unpack(f2_fma(u2_pack(s[2 * q], s[2 * q + 1]), f2, a2), y0, y1);
             y0 = fast_exp2(y0);
             y1 = fast_exp2(y1);
-            if (q & 1) l1 = f2_add(l1, f2_pack(y0, y1));
-            else l0 = f2_add(l0, f2_pack(y0, y1));
+            l0 = f2_add(l0, f2_pack(y0, y1));
             p[q] = pack2(y0, y1);
+            const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&p[q]));
+            l1 = f2_add(l1, f2_pack(back.x, back.y));
           }
           tmem_st16_async(ts + 16 * c, p);  // over scores that have been read
         }
-        float s0, s1;
-        f2_unpack(f2_add(l0, l1), s0, s1);
+        float s0, s1, r0, r1;
+        f2_unpack(l0, s0, s1);
+        f2_unpack(l1, r0, r1);
         l = fmaf(s0 + s1, un, l);
+        // (where all of a unit's p' are below 1, which is far below the largest: values of a small scale, whose p' may
+        // have lost bits that 2^-w makes matter, and whose weight in O is small)
+        lr = fmaf(unit_max < m ? s0 + s1 : r0 + r1, un, lr);
         tmem_wait_st();
         tc_fence_before();
       }
@@ -698,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
     if (!ok) *abort_flag = 1;
     // normalised output of this stream; two streams of the same rows join in the first one.  It is written out, or
     // staged over operands that are done with (B_O follows every MMA) where a cluster shares the prefix.
-    float inv = !ok ? NAN : l == 0.f ? 0.f : 1.f / l;
+    float inv = !ok ? NAN : l == 0.f ? 0.f : 1.f / lr;
     float lse = !ok ? NAN : l == 0.f ? -INFINITY : m + log2f(l);
     const bool o_on = ok && n_own > 0;  // (uniform: else O was never written)
     if (o_on) tc_fence_after();
