@@ -79,6 +79,17 @@ __global__ void __launch_bounds__(THREADS) kv8_append_kernel(Kv8View c, spec_kv8
     r = a.src_rows ? a.src_rows[j] : j;
     return (s >= 0 && s < limit && r >= 0 && r < a.n_src) ? s : -1;
   };
+  // CTAs of a few rows mostly have no run that starts in theirs
+  if (THREADS == 128) {
+    bool starts = false;
+    const int i = r0 + tid;
+    if (tid < rows_per_cta && i < a.rows) {
+      int none;
+      const int slot = slot_of(i, none);
+      starts = slot >= 0 && ((slot & (c.page - 1)) == 0 || i == 0 || slot_of(i - 1, none) != slot - 1);
+    }
+    if (!__syncthreads_or(starts)) return;
+  }
   for (int w = tid; w < ((rows_per_cta + c.page + 31) & ~31); w += THREADS) {
     const int i = r0 + w;
     int slot = -1, row = 0, before = -1, none;
@@ -114,9 +125,11 @@ __global__ void __launch_bounds__(THREADS) kv8_append_kernel(Kv8View c, spec_kv8
     uint8_t* const base = c.codes[plane] + (((size_t)pg * c.hkv + head) << c.page_log2) * kKv8Hd + col;
     const int old_byte = place > 0 ? (int)*ep : 0;
     Eight<T> held[HELD];
+    auto load = [&](int r0) {  // rows r0 .. of the run, HELD per thread in flight
 #pragma unroll
-    for (int k = 0; k < HELD; ++k)
-      if (sub + k * kRowsAtOnce < n) held[k].load(src + row_stride * s_src[i + sub + k * kRowsAtOnce]);
+      for (int k = 0; k < HELD; ++k)
+        if (r0 + sub + k * kRowsAtOnce < n) held[k].load(src + row_stride * s_src[i + r0 + sub + k * kRowsAtOnce]);
+    };
     float amax = 0.f;
     bool nan = false;
     auto look = [&](const Eight<T>& x) {
@@ -129,13 +142,12 @@ __global__ void __launch_bounds__(THREADS) kv8_append_kernel(Kv8View c, spec_kv8
         nan |= m != m;
       }
     };
+    constexpr int kBatch = HELD * kRowsAtOnce;
+    for (int r = 0; r < n; r += kBatch) {
+      load(r);
 #pragma unroll
-    for (int k = 0; k < HELD; ++k)
-      if (sub + k * kRowsAtOnce < n) look(held[k]);
-    for (int r = sub + HELD * kRowsAtOnce; r < n; r += kRowsAtOnce) {
-      Eight<T> x;
-      x.load(src + row_stride * s_src[i + r]);
-      look(x);
+      for (int k = 0; k < HELD; ++k)
+        if (r + sub + k * kRowsAtOnce < n) look(held[k]);
     }
     amax = warp_max(amax);
     nan = __any_sync(0xffffffffu, nan);
@@ -173,13 +185,11 @@ __global__ void __launch_bounds__(THREADS) kv8_append_kernel(Kv8View c, spec_kv8
       x.get(v);
       *reinterpret_cast<uint2*>(to + (size_t)r * kKv8Hd) = encode8(v, f);
     };
+    for (int r = 0; r < n; r += kBatch) {
+      if (n > kBatch) load(r);  // (a run of one batch is still there)
 #pragma unroll
-    for (int k = 0; k < HELD; ++k)
-      if (sub + k * kRowsAtOnce < n) put(sub + k * kRowsAtOnce, held[k]);
-    for (int r = sub + HELD * kRowsAtOnce; r < n; r += kRowsAtOnce) {
-      Eight<T> x;
-      x.load(src + row_stride * s_src[i + r]);
-      put(r, x);
+      for (int k = 0; k < HELD; ++k)
+        if (r + sub + k * kRowsAtOnce < n) put(r + sub + k * kRowsAtOnce, held[k]);
     }
     if (t == 0) *ep = (uint8_t)(nan ? 255 : e + 127);
     i = end;
@@ -190,15 +200,16 @@ __global__ void __launch_bounds__(THREADS) kv8_append_kernel(Kv8View c, spec_kv8
 template <typename T>
 void launch_append(const Kv8View& c, const spec_kv8_append_args& a, int per, cudaStream_t s) {
   const dim3 grid((a.rows + per - 1) / per, c.hkv);
-  if (per == 1) kv8_append_kernel<T, 64, 4><<<grid, 64, 0, s>>>(c, a, per);
+  if (per <= 4) kv8_append_kernel<T, 128, 4><<<grid, 128, 0, s>>>(c, a, per);
   else kv8_append_kernel<T, 256, 8><<<grid, 256, 0, s>>>(c, a, per);
 }
 
 }  // namespace
 
 cudaError_t launch_kv8_append(const Kv8View& c, const spec_kv8_append_args& a, int sm_count, cudaStream_t s) {
-  // One row per CTA of 64 threads while that leaves the GPU room (a decoding step, accepted rows), up to a page per CTA
-  // of 256 for prompts.  A CTA's runs are stored one after the other.
+  // A sixteenth of an SM's share of the rows per CTA, at most a page: a CTA's runs are stored one after the other.
+  // Up to four rows (decoding steps, accepted rows) CTAs have 128 threads (64 rows of bf16 and 8 heads: 3.1 us; 5.3
+  // with 256 threads), for prompts 256 (32k such rows, 195 MB: 52 us, 3.7 TB/s; 84 with 128).
   int per = (int)((long long)a.rows * c.hkv / (16 * sm_count));
   per = per < 1 ? 1 : per > c.page ? c.page : per;
   if (a.dtype == SPEC_DTYPE_F32) launch_append<float>(c, a, per, s);

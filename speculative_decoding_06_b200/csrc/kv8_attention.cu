@@ -113,7 +113,7 @@ __device__ __forceinline__ void load16(const T* p, float (&v)[16]) {
 }
 
 template <typename T, int NT>
-__global__ void __launch_bounds__(kThreads) kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8View c,
+__global__ void __launch_bounds__(kThreads, 3) kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8View c,
                                                               spec_kv8_attention_args a, DecodePlan pl) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -511,11 +511,12 @@ DecodePlan plan_decode(int hkv, int sm_count, int batch, int n_q_heads, int max_
   *nt = rows <= 8 ? 1 : 2;
   p.row_tiles = (rows + 8 * *nt - 1) / (8 * *nt);
   const long long groups = (long long)batch * hkv * p.row_tiles;
-  // Chunks of about an eighth of an SM's share of the keys (prefixes of one length assumed: ragged ones make fewer
-  // CTAs) where there are at least as many groups as SMs, for an even load (64 sequences x 8 heads: 60.5 us, 66.6 with
-  // a quarter, 63.6 with a sixteenth); of a quarter where there are fewer, since every chunk costs a partial result
-  // (7 x 4 up to 16385 tokens: 23.5 us, 29.9 with an eighth).  At least a tile for each warp.
-  const long long want = groups * max_prefix / ((groups >= sm_count ? 8LL : 4LL) * sm_count);
+  // One round of three CTAs per SM where that makes chunks of up to 1024 keys: a CTA's start, end and partial result
+  // take some 5 us.  With more work than that, shares of an eighth of an SM's keys, for an even load (prefixes of one
+  // length assumed: ragged ones make fewer CTAs).  64 sequences x 8 heads of 512 - 4096 tokens: 60.5 us with eighths,
+  // 66.6 with quarters, 63.6 with sixteenths.  At least a tile for each warp.
+  long long want = groups * max_prefix / (3LL * sm_count);
+  if (want > 1024) want = groups * max_prefix / (8LL * sm_count) > 1024 ? groups * max_prefix / (8LL * sm_count) : 1024;
   long long chunk = (want + 127) / 128 * 128;
   chunk = chunk < 128 ? 128 : chunk > kMaxChunk ? kMaxChunk : chunk;
   p.chunk = (int)chunk;

@@ -524,33 +524,48 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
     const int node = row_ok ? by_g(qr) : 0;
     const bool warp_on = __any_sync(0xffffffffu, row_ok);
     // q as fp16: bf16 rows times a power of two (see shift_of)
-    // (rolled up: code that runs once costs its instruction fetches)
+    int qex[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) qex[i] = 0;
+    if (!__is_same(T, __half)) {
+      float mq[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float v[8];
+        unpack8<T>(qraw[i], v);
+        mq[i] = fmaxf(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))),
+                      fmaxf(fmaxf(fabsf(v[4]), fabsf(v[5])), fmaxf(fabsf(v[6]), fabsf(v[7]))));  // (NaN is passed over)
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (mq[i] == INFINITY) {  // (rare) the largest of the finite values
+          mq[i] = 0.f;
 #pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t w = q == 0 ? qraw[i].x : q == 1 ? qraw[i].y : q == 2 ? qraw[i].z : qraw[i].w;
+            mq[i] = fmaxf(mq[i], fmaxf(fabsf(finite_or_0(__uint_as_float(w << 16))),
+                                       fabsf(finite_or_0(__uint_as_float(w & 0xffff0000u)))));
+          }
+        }
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mq[i] = fmaxf(mq[i], __shfl_xor_sync(0xffffffffu, mq[i], o));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) qex[i] = shift_of(mq[i]);
+    }
+#pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int qrow = 16 * warp + 2 * i + (lane >> 4);
-      int ex = 0;
-      uint4 y = qraw[0];
-#pragma unroll
-      for (int k = 0; k < 7; ++k) qraw[k] = qraw[k + 1];
+      uint4 y = qraw[i];
       if (!__is_same(T, __half)) {
         float v[8];
         unpack8<T>(y, v);
-        float m = 0.f;
-#pragma unroll
-        for (int q = 0; q < 8; q += 2) m = fmaxf(m, fmaxf(fabsf(v[q]), fabsf(v[q + 1])));  // (NaN is passed over)
-        if (m == INFINITY) {  // the largest of the finite values
-          m = 0.f;
-#pragma unroll 1
-          for (int q = 0; q < 8; ++q) m = fmaxf(m, fabsf(finite_or_0(to_f32<T>(reinterpret_cast<const T*>(&y)[q]))));
-        }
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        ex = shift_of(m);
-        y = pack8(v, pow2i(-ex));
+        y = pack8(v, pow2i(-qex[i]));
       }
-      *reinterpret_cast<uint4*>(smem + M::q + ((lane >> 3) & 1) * kQHalf + qrow * 128 +
-                                (((lane & 7) ^ (qrow & 7)) << 4)) = y;
-      if ((lane & 15) == 0) s_row[qrow] = a.scale * 1.4426950408889634f * pow2i(ex);
+      *reinterpret_cast<uint4*>(smem + M::q + ((lane >> 3) & 1) * kQHalf + qrow * 128 + (((lane & 7) ^ (qrow & 7)) << 4)) = y;
+      if ((lane & 15) == 0) s_row[qrow] = a.scale * 1.4426950408889634f * pow2i(qex[i]);
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -716,28 +731,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
     const uint32_t sw = (uint32_t)(r & 7) << 4;
     uint8_t* const stg0 = smem + M::stage + r * 512;
     uint8_t* const stg1 = stg0 + 128 * 512;
-    auto read_o = [&](int c, float (&o)[16]) {
+    auto read_o = [&](int c, float (&o)[32]) {
       if (o_on) {
-        tmem_ld16(tl + 128 + 16 * c, o);
+        uint32_t w[32];
+        tmem_ld32_async(tl + 128 + 32 * c, w);
+        tmem_wait_ld();
+        tmem_reg_fence32(w);
 #pragma unroll
-        for (int q = 0; q < 16; ++q) o[q] *= inv;
+        for (int q = 0; q < 32; ++q) o[q] = __uint_as_float(w[q]) * inv;
       } else {
 #pragma unroll
-        for (int q = 0; q < 16; ++q) o[q] = ok ? 0.f : NAN;
+        for (int q = 0; q < 32; ++q) o[q] = ok ? 0.f : NAN;
       }
     };
-    auto stage_o = [&](uint8_t* stg, int c, const float (&o)[16]) {
+    auto stage_o = [&](uint8_t* stg, int c, const float (&o)[32]) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<float4*>(stg + (((4 * c + q) << 4) ^ sw)) =
+      for (int q = 0; q < 8; ++q)
+        *reinterpret_cast<float4*>(stg + (((8 * c + q) << 4) ^ sw)) =
             make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
     };
     float w1 = 0.f;
     if (t == 1) {
       if (warp_on) {
 #pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
-          float o[16];
+        for (int c = 0; c < 4; ++c) {
+          float o[32];
           read_o(c, o);
           stage_o(stg1, c, o);
         }
@@ -757,12 +775,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
       const bool wild = nt > 0 && (s_vbad[0] | s_vbad[1] | s_vbad[2] | s_vbad[3]);
       T* out = reinterpret_cast<T*>(a.out) + a.out_row_stride * (first + node) + (size_t)(kvh * G + (qr - node * G)) * kKv8Hd;
 #pragma unroll 1
-      for (int c = 0; c < 8; ++c) {
-        float o[16];
+      for (int c = 0; c < 4; ++c) {
+        float o[32];
         read_o(c, o);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float4 y = *reinterpret_cast<const float4*>(stg1 + (((4 * c + q) << 4) ^ sw));
+        for (int q = 0; q < 8; ++q) {
+          const float4 y = *reinterpret_cast<const float4*>(stg1 + (((8 * c + q) << 4) ^ sw));
           o[4 * q] = fmaf(w1, y.x, o[4 * q]);
           o[4 * q + 1] = fmaf(w1, y.y, o[4 * q + 1]);
           o[4 * q + 2] = fmaf(w1, y.z, o[4 * q + 2]);
@@ -773,9 +791,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
           for (int k = 0; k <= top; ++k) {
             if (!(s_vbad[k >> 5] >> (k & 31) & 1u)) continue;
             if (!((k < 64 ? anc0 >> k : anc1 >> (k - 64)) & 1)) continue;
-            const T* vp = reinterpret_cast<const T*>(a.v_new) + a.v_row_stride * (first + k) + a.v_head_stride * kvh + 16 * c;
+            const T* vp = reinterpret_cast<const T*>(a.v_new) + a.v_row_stride * (first + k) + a.v_head_stride * kvh + 32 * c;
 #pragma unroll
-            for (int q = 0; q < 16; ++q) {
+            for (int q = 0; q < 32; ++q) {
               const float v = to_f32<T>(vp[q]);
               if (!(fabsf(v) < INFINITY)) o[q] += v;
             }
@@ -783,12 +801,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
         }
         if (pl.chunks == 1) {
           if (row_ok) {
-            uint4 w[2];
+            uint4 w[4];
             T* e = reinterpret_cast<T*>(w);
 #pragma unroll
-            for (int q = 0; q < 16; ++q) e[q] = from_f32<T>(o[q]);
-            reinterpret_cast<uint4*>(out + 16 * c)[0] = w[0];
-            reinterpret_cast<uint4*>(out + 16 * c)[1] = w[1];
+            for (int q = 0; q < 32; ++q) e[q] = from_f32<T>(o[q]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) reinterpret_cast<uint4*>(out + 32 * c)[q] = w[q];
           }
         } else {
           stage_o(stg0, c, o);
