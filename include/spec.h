@@ -415,7 +415,8 @@ SPEC_API int spec_lm_head_argmax_noalloc(const float* hidden, const void* final_
  * (it has to be current again at every call: SPEC_ERR_ARG otherwise), queue their
  * work on cuda_stream (NULL: the legacy default stream), do not synchronise and
  * allocate nothing; all can be captured into a CUDA graph.  Calls that touch the
- * same pages or buffers have to be ordered by the caller. */
+ * same pages or buffers have to be ordered by the caller, outputs may overlap inputs
+ * only where it is said, and a handle is not for two threads at once. */
 typedef struct spec_kv8_config {
   int32_t n_layers;
   int32_t n_kv_heads;
@@ -523,8 +524,9 @@ typedef struct spec_kv8_attention_args {
   const int32_t* seq_ids;  /* [batch], or NULL: entry b is sequence b */
   void* out;               /* [rows][n_q_heads][128], contiguous but for out_row_stride */
   float* lse;              /* [rows][n_q_heads], or NULL */
-  void* workspace;         /* spec_kv8_attention_workspace() bytes, zero before its first use; calls that may
-                              overlap on the GPU need one each */
+  void* workspace;         /* spec_kv8_attention_workspace() bytes, zero before its first use, then for calls of
+                              any bounds that it is large enough for; calls (or graphs) that may overlap on the
+                              GPU need one each */
   size_t workspace_bytes;
   int64_t q_row_stride, q_head_stride, k_row_stride, k_head_stride, v_row_stride, v_head_stride,
       out_row_stride;      /* in elements; rows of 16-byte alignment */

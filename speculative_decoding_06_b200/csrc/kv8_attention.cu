@@ -50,11 +50,15 @@ constexpr int kTileBytes = kTile * 2 * kKv8Hd;
 constexpr int kMaxChunk = 4096;    // keys of a CTA: its page ids and scales lie in shared memory
 constexpr int kGroups = kMaxChunk / 16;
 
+// Workspace: arrival counters at its start, wherever a call's bounds put the rest, so that they are zero between calls
+// of any bounds; then (m, l) and O of every (group, chunk).
+constexpr int kMaxGroups = 16384;  // groups (sequence, kv head, row tile) of one launch
 struct DecodePlan {
   int chunk, chunks, row_tiles;
-  float* part;   // [group][chunk][rows][128], then (m, l) [group][chunk][rows]
-  float2* ml;
-  int* counters; // [group]
+  int group0, groups;  // of this launch, of all
+  int* counters;       // [kMaxGroups]
+  float2* ml;          // [group][chunk][rows]
+  float* part;         // [group][chunk][rows][128]
 };
 
 struct Smem {
@@ -126,8 +130,8 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_decode_kernel(const __grid_co
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int G = a.n_q_heads / c.hkv;
-  const int group = blockIdx.x / pl.chunks, chunk_i = blockIdx.x - group * pl.chunks;
-  const int bk = group / pl.row_tiles, row0 = (group - bk * pl.row_tiles) * kRows;
+  const int group = blockIdx.x / pl.chunks, chunk_i = blockIdx.x - group * pl.chunks;  // (group of the launch)
+  const int bk = (pl.group0 + group) / pl.row_tiles, row0 = (pl.group0 + group - bk * pl.row_tiles) * kRows;
   const int b = bk / c.hkv, kvh = bk - b * c.hkv;
   const int first = a.offsets[b], n = a.offsets[b + 1] - first;
   const int seq = a.seq_ids ? a.seq_ids[b] : b;
@@ -267,8 +271,12 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_decode_kernel(const __grid_co
 
   bool landed = true;
   for (int i = 0; i < mine; ++i) {
-    landed = mbar_wait(&full[i % kStages], (i / kStages) & 1, nullptr, nullptr) && landed;
-    landed = __all_sync(0xffffffffu, landed);
+    landed = __all_sync(0xffffffffu, mbar_wait(&full[i % kStages], (i / kStages) & 1, nullptr, nullptr));
+    if (!landed) {  // a wait ran out: copies under way land before the CTA's memory is released, and the rows say so
+      for (int k = i + 1; k < min(mine, i + kStages); ++k)
+        mbar_wait(&full[k % kStages], (k / kStages) & 1, nullptr, nullptr);
+      break;
+    }
     const uint8_t* const buf = ring + (i % kStages) * kTileBytes;
     auto piece = [&](int at) { return *reinterpret_cast<const uint4*>(buf + at); };
     const int g0 = 2 * (warp + kWarps * i);
@@ -362,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_decode_kernel(const __grid_co
     __syncwarp();  // every lane has used what it read: the stage may be filled again
     fetch(i + kStages);
   }
-  if (!landed) {  // a wait ran out: the rows say so
+  if (!landed) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) l[nt][0] = l[nt][1] = NAN;
   }
@@ -522,12 +530,12 @@ DecodePlan plan_decode(int hkv, int sm_count, int batch, int n_q_heads, int max_
   p.chunk = (int)chunk;
   p.chunks = (int)((max_prefix + chunk - 1) / chunk);
   if (p.chunks < 1) p.chunks = 1;
-  size_t n = 16;
-  if (p.chunks > 1) {
-    const size_t slots = (size_t)groups * p.chunks * 8 * *nt;
-    n = (4 * (size_t)groups + 255) / 256 * 256 + slots * (kKv8Hd * 4 + 8);
-  }
-  *bytes = n;
+  p.groups = (int)groups;
+  // (a launch's grid stays below 2^30)
+  const int per_launch = p.chunks > (1 << 30) / kMaxGroups ? (1 << 30) / p.chunks : kMaxGroups;
+  const size_t slots = (size_t)(groups < per_launch ? groups : per_launch) * p.chunks * 8 * *nt;
+  p.group0 = per_launch;
+  *bytes = p.chunks > 1 ? 4 * kMaxGroups + slots * (kKv8Hd * 4 + 8) : 16;
   return p;
 }
 
@@ -559,20 +567,24 @@ cudaError_t launch_kv8_attention(const Kv8View& c, const CUtensorMap& map, const
   int nt = 1;
   size_t bytes = 0;
   DecodePlan p = plan_decode(c.hkv, sm_count, a.batch, a.n_q_heads, a.max_nodes, a.max_prefix, &nt, &bytes);
-  const size_t groups = (size_t)a.batch * c.hkv * p.row_tiles;
+  const int per_launch = p.group0;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   p.counters = reinterpret_cast<int*>(ws);
-  p.ml = reinterpret_cast<float2*>(ws + (4 * groups + 255) / 256 * 256);
-  p.part = reinterpret_cast<float*>(p.ml + groups * p.chunks * 8 * nt);
-  const unsigned grid = (unsigned)(groups * p.chunks);
-  if (a.dtype == SPEC_DTYPE_BF16) {
-    if (nt == 1) kv8_decode_kernel<__nv_bfloat16, 1><<<grid, kThreads, Smem::dyn, s>>>(map, c, a, p);
-    else kv8_decode_kernel<__nv_bfloat16, 2><<<grid, kThreads, Smem::dyn, s>>>(map, c, a, p);
-  } else {
-    if (nt == 1) kv8_decode_kernel<__half, 1><<<grid, kThreads, Smem::dyn, s>>>(map, c, a, p);
-    else kv8_decode_kernel<__half, 2><<<grid, kThreads, Smem::dyn, s>>>(map, c, a, p);
+  p.ml = reinterpret_cast<float2*>(ws + 4 * kMaxGroups);
+  p.part = reinterpret_cast<float*>(p.ml + (size_t)(p.groups < per_launch ? p.groups : per_launch) * p.chunks * 8 * nt);
+  for (p.group0 = 0; p.group0 < p.groups; p.group0 += per_launch) {
+    const unsigned grid = (unsigned)(p.groups - p.group0 < per_launch ? p.groups - p.group0 : per_launch) * p.chunks;
+    if (a.dtype == SPEC_DTYPE_BF16) {
+      if (nt == 1) kv8_decode_kernel<__nv_bfloat16, 1><<<grid, kThreads, Smem::dyn, s>>>(map, c, a, p);
+      else kv8_decode_kernel<__nv_bfloat16, 2><<<grid, kThreads, Smem::dyn, s>>>(map, c, a, p);
+    } else {
+      if (nt == 1) kv8_decode_kernel<__half, 1><<<grid, kThreads, Smem::dyn, s>>>(map, c, a, p);
+      else kv8_decode_kernel<__half, 2><<<grid, kThreads, Smem::dyn, s>>>(map, c, a, p);
+    }
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
   }
-  return cudaGetLastError();
+  return cudaSuccess;
 }
 
 }  // namespace spec

@@ -415,3 +415,68 @@ def test_refusals_of_the_torch_side():
         cache.append(0, c["k"].cuda(), c["v"].cuda(), i32([0, 1, 2]))
     with pytest.raises(ValueError):
         cache.plan(i32([0]), i32([1]), i32([[0]]), i32([0]), i32([0, 1]), 4)  # the ring holds every page
+
+
+def test_workspace_serves_calls_of_other_bounds():
+    """One workspace, used for many sequences, then for few, then for many: the counters are where every call looks."""
+    big = attention_case(21, [700 + 5 * i for i in range(20)], [1] * 20, 4, 2, 32, "bf16")
+    small = attention_case(22, [1500, 3], [2, 1], 4, 1, 64, "bf16")
+    ws = big["cache"].attention_workspace(64, 8, 4, 4096)
+    refs = [reference(c) for c in (big, small)]
+    for _ in range(3):
+        for c, ref in zip((big, small), refs):
+            check_attention(c, run_attention(c, workspace=ws), ref)
+    with pytest.raises(S.SpecError):
+        run_attention(big, workspace=ws[:1000])
+
+
+@pytest.mark.parametrize("nodes", [[20, 3], [128, 40]])
+def test_many_rows_with_a_bound_beyond_the_tensor_core_kernel(nodes):
+    """max_prefix above what the cluster kernel numbers: the streaming kernel takes the rows in tiles."""
+    c = attention_case(23, [200, 90], nodes, 4, 1, 128, "fp16")
+    wide = np.full((c["tables"].shape[0], 4000), -1, np.int32)
+    wide[:, :c["tables"].shape[1]] = c["tables"]
+    c["tables"] = wide
+    check_attention(c, run_attention(c, max_prefix=500000), reference(c))
+
+
+def test_more_groups_than_one_launch_takes():
+    """2500 sequences of 8 kv heads, long and short ones on shared pages, in chunks: several launches, one workspace."""
+    c = attention_case(24, [4600, 130], [1, 1], 8, 8, 64, "bf16", extra_seqs=0, tree="none")
+    reps = 1250
+    order = np.concatenate([np.arange(2)] * reps)
+    tables, lengths = c["tables"][c["ids"]][order], c["lengths"][c["ids"]][order]
+    lengths[2::2] = 70  # the first of them long, the last too
+    lengths[-2] = 4600
+    q = c["q"].cuda()[torch.from_numpy(order).cuda()]
+    out, lse = c["cache"].attention(0, q, i32(tables), i32(lengths), i32(np.arange(2 * reps + 1)), max_prefix=4600,
+                                    max_nodes=1)
+    ref = reference(c)
+    check_attention(c, (out[:2], lse[:2]), ref)
+    check_attention(c, (out[-2:], lse[-2:]), ref)
+    assert torch.equal(out[1::2], out[1:2].expand(reps, -1, -1)) and torch.equal(lse[1::2], lse[1:2].expand(reps, -1))
+    assert torch.equal(out[2:-2:2], out[2:3].expand(reps - 2, -1, -1))
+
+
+@pytest.mark.parametrize("nodes", [1, 40])
+def test_pages_beyond_32_bit_offsets(nodes):
+    """A cache of more than 2^32 bytes a plane: its last pages, written, read and attended to."""
+    from speculative_decoding_06_b200.kv8 import KV8Cache
+    hkv, page, n_pages = 8, 64, 66000
+    cache = KV8Cache(1, hkv, n_pages, page)
+    assert cache.codes[0, 0].numel() > 1 << 32
+    g = np.random.default_rng(nodes)
+    P = 100
+    k, v = (torch.from_numpy(g.normal(size=(P, hkv, 128))).to(torch.bfloat16) for _ in range(2))
+    used = [n_pages - 1, n_pages - 3]
+    slots = [used[j // page] * page + j % page for j in range(P)]
+    cache.append(0, k.cuda(), v.cuda(), i32(slots))
+    codes, exps = np.zeros((2, 2, hkv, page, 128), np.uint8), np.zeros((2, 2, hkv), np.uint8)
+    O.append(codes, exps, page, k.double().numpy(), v.double().numpy(), list(range(P)))
+    got = cache.codes[0][:, used].cpu().numpy()
+    assert np.array_equal(got[:, 0], codes[:, 0]) and np.array_equal(got[:, 1, :, :P - page], codes[:, 1, :, :P - page])
+    c = dict(cache=cache, codes=codes, exps=exps, page=page, dtype="bf16",
+             q=torch.from_numpy(g.normal(size=(nodes, hkv, 128))).to(torch.bfloat16))
+    out = cache.attention(0, c["q"].cuda(), i32([used]), i32([P]), i32([0, nodes]), max_prefix=P, max_nodes=nodes)
+    check_attention(c, out, O.attention(codes, exps, page, c["q"].double().numpy(), np.array([[0, 1]]), [P], [0, nodes],
+                                        128 ** -0.5))
