@@ -63,10 +63,13 @@ constexpr int kLoadWarp = kIssueWarp + 2;
 constexpr int kThreads = 32 * (kLoadWarp + 1);
 constexpr int kStages = 4;    // most operand stages of K or V
 
-// mbarriers: per operand stage; S, P and P V per stream and buffer
+constexpr int kByLength = 128;  // most sequences that are put in order
+constexpr int kScores = 3;    // S buffers: unit u has buffer u % 3
+
+// mbarriers: per operand stage; S, P and P V per S buffer; P V also per stream
 enum { B_Q = 0, B_O = 1, B_TREF = 2, B_DRAIN = 4, B_KFULL = 6, B_KEMPTY = B_KFULL + kStages, B_VFULL = B_KEMPTY + kStages,
-       B_VEMPTY = B_VFULL + kStages, B_SFULL = B_VEMPTY + kStages, B_PFULL = B_SFULL + 4, B_PV = B_PFULL + 4,
-       B_CFULL = B_PV + 4, B_CEMPTY = B_CFULL + 2 * kCodeStages, kNumBars = B_CEMPTY + 2 * kCodeStages };
+       B_VEMPTY = B_VFULL + kStages, B_SFULL = B_VEMPTY + kStages, B_PFULL = B_SFULL + kScores, B_PV = B_PFULL + kScores,
+       B_OUT = B_PV + kScores, B_CFULL = B_OUT + 2, B_CEMPTY = B_CFULL + 2 * kCodeStages, kNumBars = B_CEMPTY + 2 * kCodeStages };
 
 struct M {  // shared memory
   static constexpr int nk = 3;             // operand stages (units) of K
@@ -93,13 +96,18 @@ struct M {  // shared memory
 static_assert(M::dyn <= 227 * 1024, "shared memory");
 static_assert(M::codes - M::stage >= 2 * 128 * 512, "staging");
 
-// TMEM columns of stream t: two S buffers of 64 at 256 t, O at 256 t + 128.  P lies over the first half of its S.
+// TMEM columns: O of the streams, the S buffers (P lies over the first half of its S), q as the scores' A operand.
+// (q in shared memory would be read again for every unit: 256 of the 1024 cycles that a unit then takes of the
+// shared-memory pipe.)
 constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 256, kColQ = kColS + kScores * kKeys;
+static_assert(kColQ + 64 <= kTmemCols, "tensor memory");
 constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kKeys >> 3) << 17) | ((uint32_t)(kRowTile >> 4) << 24);
 constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | ((uint32_t)(128 >> 3) << 17) | ((uint32_t)(kRowTile >> 4) << 24);
 
 struct TcPlan {
   int chunks;          // CTAs of a cluster
+  bool by_length;      // blocks of the longest prefixes first
   uint32_t by_chunks;  // ceil(2^32 / chunks): x / chunks = x * by_chunks >> 32 for x < 2^29
   uint32_t by_group;   // ceil(2^20 / G): x / G = x * by_group >> 20 for x <= 128 * 64
 };
@@ -170,6 +178,13 @@ __device__ __forceinline__ bool finite_only(uint4& r) {
   return any;
 }
 
+// a + c, a in 16 bits
+__device__ __forceinline__ float add_half(float c, uint16_t a) {
+  float d;
+  asm("add.f32.f16 %0, %1, %2;" : "=f"(d) : "h"(a), "f"(c));
+  return d;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_kv8_attention_args a, TcPlan pl) {
   extern __shared__ uint8_t smem_raw[];
@@ -189,7 +204,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
   // cluster differ in `share` only: they return together or not at all
   const int share = pl.chunks > 1 ? (int)cluster_rank() : 0;
   const int row0 = (pl.chunks > 1 ? (int)cluster_id_x() : (int)blockIdx.x) * kRowTile;
-  const int b = blockIdx.z, kvh = blockIdx.y;
+  const int kvh = blockIdx.y;
+  int b = blockIdx.z;
+  if (pl.by_length) {  // blocks start in order: the longest prefixes first
+    int* len = reinterpret_cast<int*>(s_row);
+    if (tid < a.batch) {
+      const int s = a.seq_ids ? a.seq_ids[tid] : tid;
+      len[tid] = s < 0 || s >= a.n_seqs ? -1 : a.lengths[s];
+    }
+    __syncthreads();
+    if (tid < a.batch) {
+      const int own = len[tid];
+      int rank = 0;
+      for (int i = 0; i < a.batch; ++i) rank += len[i] > own || (len[i] == own && i < tid);
+      if (rank == b) len[kByLength] = tid;
+    }
+    __syncthreads();
+    b = len[kByLength];
+  }
   const int first = a.offsets[b], n = a.offsets[b + 1] - first;
   const int seq = a.seq_ids ? a.seq_ids[b] : b;
   if (seq < 0 || seq >= a.n_seqs || first < 0 || n < 1 || n > a.max_nodes || n > a.rows - first) return;
@@ -262,11 +294,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
       mbar_init(&bar[B_CFULL + s], 1);
       mbar_init(&bar[B_CEMPTY + s], kConvWarps);
     }
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < kScores; ++s) {
       mbar_init(&bar[B_SFULL + s], 1);
       mbar_init(&bar[B_PFULL + s], 4);
       mbar_init(&bar[B_PV + s], 1);
     }
+    for (int s = 0; s < 2; ++s) mbar_init(&bar[B_OUT + s], 1);
     for (int s = 0; s < 2; ++s) mbar_init(&bar[B_TREF + s], 2 * kConvWarps);
     mbar_init(&bar[B_O], 2);
     mbar_init(&bar[B_DRAIN], 1);
@@ -320,41 +353,40 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
     // ------------------------------------------------------------ MMA issue, stream t
     const int t = warp - kIssueWarp;
     if (elect_one()) {
-      const uint64_t dq = sw128_kmajor_desc(smem_u32(smem + M::q));
       const uint64_t dk = sw128_kmajor_desc(smem_u32(smem + M::k));
       const uint64_t dv = sw128_mnmajor_desc(smem_u32(smem + M::v), kHalf);
-      const uint32_t col = tmem + 256 * t;
       const int n_own = (nu - t + 1) >> 1;  // units t, t + 2, ...
       int ks_ = t, kp = 0, vs = t, vp = 0;  // operand stages of K and V, and their phases
+      int sb = t, sp = 0, pb = t, pp = 0;   // S buffer of the next scores and of the next product, and their phases
       bool ok = held(B_Q, 0);
       for (int i = 0; i <= n_own && ok; ++i) {
         if (i < n_own) {
-          const int sb = 2 * t + (i & 1);
-          // the S buffer holds P of the stream's unit before the last until that one's product is done
-          if (i >= 2) ok = held(B_PV + sb, ((i - 2) >> 1) & 1);
-          ok = ok && held(B_KFULL + ks_, kp);
+          // the S buffer holds P of three units ago until that one's product is done
+          ok = held(B_PV + sb, sp ^ 1) && held(B_KFULL + ks_, kp);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)  // 16 dimensions per step (a descriptor's low bits count 16 bytes)
-            tc_mma_bf16(col + kKeys * (i & 1), dq + (((ks >> 2) * kQHalf + (ks & 3) * 32) >> 4),
-                        dk + ((ks_ * kUnit + (ks >> 2) * kHalf + (ks & 3) * 32) >> 4), kIdescS, ks > 0 ? 1u : 0u);
+          for (int ks = 0; ks < 8; ++ks)  // 16 dimensions per step: 8 columns of q (a descriptor's low bits count 16 bytes)
+            tc_mma_ts(tmem + kColS + kKeys * sb, tmem + kColQ + 8 * ks,
+                      dk + ((ks_ * kUnit + (ks >> 2) * kHalf + (ks & 3) * 32) >> 4), kIdescS, ks > 0 ? 1u : 0u);
           tc_commit(&bar[B_SFULL + sb]);
           tc_commit(&bar[B_KEMPTY + ks_]);
           if ((ks_ += 2) >= M::nk) ks_ -= M::nk, kp ^= 1;
+          if ((sb += 2) >= kScores) sb -= kScores, sp ^= 1;
         }
         if (i > 0) {  // O += P V of the unit before
-          const int pb = 2 * t + ((i - 1) & 1);
-          ok = held(B_VFULL + vs, vp) && held(B_PFULL + pb, ((i - 1) >> 1) & 1);
+          ok = held(B_VFULL + vs, vp) && held(B_PFULL + pb, pp);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)  // 16 keys per step: 8 columns of P
-            tc_mma_ts(col + 128, col + kKeys * ((i - 1) & 1) + kk * 8, dv + ((vs * kUnit + kk * 16 * 128) >> 4), kIdescPV,
-                      (i > 1 || kk > 0) ? 1u : 0u);
+            tc_mma_ts(tmem + 128 * t, tmem + kColS + kKeys * pb + kk * 8, dv + ((vs * kUnit + kk * 16 * 128) >> 4),
+                      kIdescPV, (i > 1 || kk > 0) ? 1u : 0u);
           tc_commit(&bar[B_PV + pb]);
+          tc_commit(&bar[B_OUT + t]);
           tc_commit(&bar[B_VEMPTY + vs]);
           if ((vs += 2) >= M::nv) vs -= M::nv, vp ^= 1;
+          if ((pb += 2) >= kScores) pb -= kScores, pp ^= 1;
         }
       }
       if (ok) {
@@ -567,9 +599,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
       *reinterpret_cast<uint4*>(smem + M::q + ((lane >> 3) & 1) * kQHalf + qrow * 128 + (((lane & 7) ^ (qrow & 7)) << 4)) = y;
       if ((lane & 15) == 0) s_row[qrow] = a.scale * 1.4426950408889634f * pow2i(qex[i]);
     }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&bar[B_Q]);
     // ancestors: each node's set doubles its reach per round (128 nodes: seven rounds)
     uint64_t anc0 = 0, anc1 = 0;
     {
@@ -580,6 +609,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
         jump[tid] = parent < tid && parent >= 0 ? parent : -1;
       }
       sync_rows();
+      {  // this thread's row of q, dimensions 64 t .., into tensor memory
+        uint32_t w[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 y = *reinterpret_cast<const uint4*>(smem + M::q + t * kQHalf + r * 128 + ((i ^ (r & 7)) << 4));
+          w[4 * i] = y.x, w[4 * i + 1] = y.y, w[4 * i + 2] = y.z, w[4 * i + 3] = y.w;
+        }
+        tmem_st32_async(tmem + ((uint32_t)((warp & 3) * 32) << 16) + kColQ + 32 * t, w);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[B_Q]);
+      }
       int cur = 0;
       if (nt > 0 && a.parents) {
         for (int reach = 1; reach <= top; reach *= 2) {
@@ -610,14 +652,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
       }
     }
     const float qs = s_row[r];
-    const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256 * t;  // this warp's lanes, the stream's columns
+    const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);  // this warp's lanes
+    const uint32_t to = tl + 128 * t;                                 // the stream's O
+    int sb = t, sp = 0;                                               // the unit's S buffer, its phase
     const int n_own = (nu - t + 1) >> 1;  // the stream's units
     float m = -INFINITY, l = 0.f, lr = 0.f;  // lr: of the rounded probabilities
     bool ok = true;
 #pragma unroll 1
     for (int i = 0; i < n_own; ++i) {
-      const int u = 2 * i + t, sb = 2 * t + (i & 1);
-      const uint32_t ts = tl + kKeys * (i & 1);
+      const int u = 2 * i + t;
+      const uint32_t ts = tl + kColS + kKeys * sb;
       uint64_t see = ~0ull;  // keys of the unit that the row sees
       if (u >= np - 1) {
         if (u >= np) {
@@ -631,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
       const float2 e = s_unit[u];
       const float f = qs * e.x, ve = e.y;
       const float un = fast_exp2(-ve);
-      if (ok) ok = held(B_SFULL + sb, (i >> 1) & 1);
+      if (ok) ok = held(B_SFULL + sb, sp);
       ok = __all_sync(0xffffffffu, ok);
       if (ok && warp_on) {
         tc_fence_after();
@@ -671,16 +715,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
           lr *= keep;
           if (i > 0) {
             // O shrinks: the product of the stream's last unit has to be in it
-            ok = __all_sync(0xffffffffu, held(B_PV + (sb ^ 1), ((i - 1) >> 1) & 1));
+            ok = __all_sync(0xffffffffu, held(B_OUT + t, (i - 1) & 1));
             if (ok) {
               tc_fence_after();
 #pragma unroll 1
               for (int c = 0; c < 8; ++c) {
                 float o[16];
-                tmem_ld16(tl + 128 + 16 * c, o);
+                tmem_ld16(to + 16 * c, o);
 #pragma unroll
                 for (int q = 0; q < 16; ++q) o[q] *= keep;
-                tmem_st16_async(tl + 128 + 16 * c, reinterpret_cast<const uint32_t*>(o));
+                tmem_st16_async(to + 16 * c, reinterpret_cast<const uint32_t*>(o));
               }
               tmem_wait_st();
             }
@@ -688,7 +732,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
         }
         const float add = ve - (m == -INFINITY ? 0.f : m);
         const uint64_t f2 = f2_pack(f, f), a2 = f2_pack(add, add);
-        uint64_t l0 = f2_pack(0.f, 0.f), l1 = l0;
+        uint64_t l0 = f2_pack(0.f, 0.f);
+        float r0 = 0.f, r1 = 0.f;  // of the rounded probabilities
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t s[32], p[16];
@@ -701,14 +746,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
             y1 = fast_exp2(y1);
             l0 = f2_add(l0, f2_pack(y0, y1));
             p[q] = pack2(y0, y1);
-            const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&p[q]));
-            l1 = f2_add(l1, f2_pack(back.x, back.y));
+            r0 = add_half(r0, (uint16_t)(p[q] & 0xffffu));
+            r1 = add_half(r1, (uint16_t)(p[q] >> 16));
           }
           tmem_st16_async(ts + 16 * c, p);  // over scores that have been read
         }
-        float s0, s1, r0, r1;
+        float s0, s1;
         f2_unpack(l0, s0, s1);
-        f2_unpack(l1, r0, r1);
         l = fmaf(s0 + s1, un, l);
         // (where all of a unit's p' are below 1, which is far below the largest: values of a small scale, whose p' may
         // have lost bits that 2^-w makes matter, and whose weight in O is small)
@@ -718,6 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar[B_PFULL + sb]);
+      if ((sb += 2) >= kScores) sb -= kScores, sp ^= 1;
     }
     if (ok && nu > 0) ok = held(B_O, 0);
     ok = __all_sync(0xffffffffu, ok);
@@ -734,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
     auto read_o = [&](int c, float (&o)[32]) {
       if (o_on) {
         uint32_t w[32];
-        tmem_ld32_async(tl + 128 + 32 * c, w);
+        tmem_ld32_async(to + 32 * c, w);
         tmem_wait_ld();
         tmem_reg_fence32(w);
 #pragma unroll
@@ -921,6 +966,7 @@ cudaError_t launch_kv8_tree(const Kv8View& c, const spec_kv8_attention_args& a, 
   chunks = chunks < 1 ? 1 : chunks > kKv8TcMaxChunks ? kKv8TcMaxChunks : chunks;
   const int need = (a.max_prefix + kKv8TcMaxKeys - 1) / kKv8TcMaxKeys;
   TcPlan p;
+  p.by_length = a.batch > 1 && a.batch <= kByLength && tiles > sm_count;
   p.chunks = chunks < need ? need : (int)chunks;
   p.by_chunks = (uint32_t)((((uint64_t)1 << 32) + p.chunks - 1) / p.chunks);
   p.by_group = (uint32_t)(((1u << 20) + G - 1) / G);
