@@ -47,31 +47,69 @@ struct Eight {
   }
 };
 
+// The largest magnitude of the values seen, as the bits of T without the sign (which are in the order of the
+// magnitudes, infinity and NaN above all others).
+template <typename T>
+struct Top {
+  uint32_t m = 0;  // a pair of 16-bit values
+  __device__ __forceinline__ void see(const Eight<T>& x) {
+    const uint4& w = x.w[0];
+    m = max2(max2(m, w.x), max2(w.y, max2(w.z, w.w)));
+  }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    using T2 = std::conditional_t<__is_same(T, __half), __half2, __nv_bfloat162>;
+    a &= 0x7fff7fffu, b &= 0x7fff7fffu;
+    const T2 c = __hmax2_nan(reinterpret_cast<const T2&>(a), reinterpret_cast<const T2&>(b));
+    return reinterpret_cast<const uint32_t&>(c);
+  }
+  __device__ __forceinline__ uint32_t bits() const { return max(m & 0x7fffu, m >> 16 & 0x7fffu); }
+  static __device__ __forceinline__ bool finite(uint32_t b) { return b < (__is_same(T, __half) ? 0x7c00u : 0x7f80u); }
+  static __device__ __forceinline__ float value(uint32_t b) {
+    const uint16_t h = (uint16_t)b;
+    return to_f32<T>(reinterpret_cast<const T&>(h));
+  }
+};
+template <>
+struct Top<float> {
+  uint32_t m = 0;
+  __device__ __forceinline__ void see(const Eight<float>& x) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(x.w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7fffffffu);
+  }
+  __device__ __forceinline__ uint32_t bits() const { return m; }
+  static __device__ __forceinline__ bool finite(uint32_t b) { return b < 0x7f800000u; }
+  static __device__ __forceinline__ float value(uint32_t b) { return __uint_as_float(b); }
+};
+
 // eight values times `s` as e4m3, round to nearest even, saturating
 __device__ __forceinline__ uint2 encode8(const float* v, float s) {
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i] * s, v[2 * i + 1] * s), __NV_SATFINITE, __NV_E4M3);
+  for (int i = 0; i < 4; ++i) {
+    float2 y;
+    f2_unpack(f2_mul(f2_pack(v[2 * i], v[2 * i + 1]), f2_pack(s, s)), y.x, y.y);
+    w[i] = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+  }
   return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
 // THREADS: half of them for K, half for V.  HELD rows per thread stay in registers, so that runs of
-// HELD * THREADS / 32 rows are read once.
-template <typename T, int THREADS, int HELD>
-__global__ void __launch_bounds__(THREADS) kv8_append_kernel(Kv8View c, spec_kv8_append_args a, int rows_per_cta) {
+// HELD * THREADS / 32 rows are read once.  CTAS: on an SM at a time.
+template <typename T, int THREADS, int HELD, int CTAS>
+__global__ void __launch_bounds__(THREADS, CTAS) kv8_append_kernel(Kv8View c, spec_kv8_append_args a, int rows_per_cta) {
   constexpr int kPlane = THREADS / 2, kRowsAtOnce = kPlane / kLanes, kWarps = kPlane / 32;
   __shared__ uint32_t s_break[9];  // rows r0 .. r0 + 255: does a run end before this row?
   __shared__ int s_slot[256], s_src[256];
   __shared__ float part[2 * kWarps];
   __shared__ int part_nan[2 * kWarps];
   const int tid = threadIdx.x, plane = tid / kPlane, t = tid % kPlane;
-  const int head = blockIdx.y;
+  const int tile = blockIdx.x, head = blockIdx.y;
   const int sub = t / kLanes, col = (t % kLanes) * 8;
   const T* src = reinterpret_cast<const T*>(plane ? a.v : a.k) + (plane ? a.v_head_stride : a.k_head_stride) * head + col;
   const int64_t row_stride = plane ? a.v_row_stride : a.k_row_stride;
   const int limit = c.n_pages << c.page_log2;
-  const int r0 = blockIdx.x * rows_per_cta;
+  const int r0 = tile * rows_per_cta;
   // The runs that start in rows r0 .. r0 + rows_per_cta - 1 (at most a page) are this CTA's; the last of them ends
   // within a page from there.  A row that stores nothing has slot -1.
   auto slot_of = [&](int j, int& r) {
@@ -145,9 +183,18 @@ __global__ void __launch_bounds__(THREADS) kv8_append_kernel(Kv8View c, spec_kv8
     constexpr int kBatch = HELD * kRowsAtOnce;
     for (int r = 0; r < n; r += kBatch) {
       load(r);
+      Top<T> top;
 #pragma unroll
       for (int k = 0; k < HELD; ++k)
-        if (r + sub + k * kRowsAtOnce < n) look(held[k]);
+        if (r + sub + k * kRowsAtOnce < n) top.see(held[k]);
+      const uint32_t bits = top.bits();
+      if (Top<T>::finite(bits)) {
+        amax = fmaxf(amax, Top<T>::value(bits));
+      } else {  // (rare) value by value
+#pragma unroll
+        for (int k = 0; k < HELD; ++k)
+          if (r + sub + k * kRowsAtOnce < n) look(held[k]);
+      }
     }
     amax = warp_max(amax);
     nan = __any_sync(0xffffffffu, nan);
@@ -200,16 +247,16 @@ __global__ void __launch_bounds__(THREADS) kv8_append_kernel(Kv8View c, spec_kv8
 template <typename T>
 void launch_append(const Kv8View& c, const spec_kv8_append_args& a, int per, cudaStream_t s) {
   const dim3 grid((a.rows + per - 1) / per, c.hkv);
-  if (per <= 4) kv8_append_kernel<T, 128, 4><<<grid, 128, 0, s>>>(c, a, per);
-  else kv8_append_kernel<T, 256, 8><<<grid, 256, 0, s>>>(c, a, per);
+  if (per <= 4) kv8_append_kernel<T, 128, 4, 1><<<grid, 128, 0, s>>>(c, a, per);
+  else kv8_append_kernel<T, 256, 8, sizeof(T) == 2 ? 4 : 2><<<grid, 256, 0, s>>>(c, a, per);
 }
 
 }  // namespace
 
 cudaError_t launch_kv8_append(const Kv8View& c, const spec_kv8_append_args& a, int sm_count, cudaStream_t s) {
   // A sixteenth of an SM's share of the rows per CTA, at most a page: a CTA's runs are stored one after the other.
-  // Up to four rows (decoding steps, accepted rows) CTAs have 128 threads (64 rows of bf16 and 8 heads: 3.1 us; 5.3
-  // with 256 threads), for prompts 256 (32k such rows, 195 MB: 52 us, 3.7 TB/s; 84 with 128).
+  // Up to four rows (decoding steps, accepted rows) CTAs have 128 threads (64 rows of bf16 and 8 heads: 3.3 us; 5.3
+  // with 256 threads), for prompts 256 (32k such rows, 195 MB: 42 us, 4.6 TB/s; 84 with 128).
   int per = (int)((long long)a.rows * c.hkv / (16 * sm_count));
   per = per < 1 ? 1 : per > c.page ? c.page : per;
   if (a.dtype == SPEC_DTYPE_F32) launch_append<float>(c, a, per, s);
