@@ -120,7 +120,8 @@ template <typename T, int NT>
 __global__ void __launch_bounds__(kThreads, 3) kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8View c,
                                                               spec_kv8_attention_args a, DecodePlan pl) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (to a 1024-byte boundary by an offset, so that the compiler still knows what it points to as shared memory)
+  uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
   int* s_page = reinterpret_cast<int*>(smem + Smem::page);
   float* s_kscale = reinterpret_cast<float*>(smem + Smem::kscale);
   float* s_vexp = reinterpret_cast<float*>(smem + Smem::vexp);

@@ -11,20 +11,23 @@
 //   converters (4 warps for K, 4 for V)  turn codes into fp16 (exact) and write them as
 //       the swizzled K and V operands.  K and V of the step's own rows become fp16
 //       times a power of two that their largest value sets.
-//   issuers (1 thread per stream)  S = Q K^T (M 128, N 64) into one of two TMEM buffers and
-//       O += P V (P from TMEM, V MN-major); scores run a unit ahead of products.
+//   issuers (1 thread per stream)  S = Q K^T (M 128, N 64) with q in TMEM, into one of three
+//       TMEM buffers, and O += P V (P from TMEM, V MN-major); scores run a unit ahead of products.
 //   softmax (4 warps per stream)  a thread per row: the online softmax in base 2, P as
 //       fp16 over the S that it came from.
 //
-// What bounds it: a unit takes 0.72 us of a CTA, 1350 cycles, of which the MMAs need
-// 512, the exponentials 512 of the special-function units and the conversions 512 of
-// the integer pipe; the rest is the latency of a unit's chain (codes to operand,
-// tensor memory to registers and back, six barriers).  Tried and slower: one issuer for both
-// streams, which keeps them in step, so that both want the special-function units at once (0.95 us);
-// codes by cp.async of the converters (0.95 us); four threads per row, whose exchange of
-// maxima costs what it saves (0.97 us); 128-key score tiles (0.97 us).  Two row tiles
-// that share a unit's conversion took 1.28 us a unit, 11 % less per row, but need twice the
-// rows.  Start and end of a CTA take about 10 us.
+// What bounds it: a unit takes 0.59 us of a CTA, 1050 cycles, of which the MMAs need
+// 512, the exponentials 512 of the special-function units, shared memory 770 (codes in and out, operands in and out)
+// and the instructions of softmax and conversion some 700 of the issue slots; the rest is the latency of a unit's
+// chain (codes to operand, tensor memory to registers and back, six barriers).  Start and end of a CTA take 13 us.
+// 4 prompts of 6150 - 8192 tokens, 128 rows x 8 kv heads x 4: 89 us, 700 TFLOP/s.
+// Tried and slower: one issuer for both streams, which keeps them in step, so that both want the special-function
+// units at once (0.95 us a unit); codes by cp.async of the converters (0.95 us); four threads per row, whose
+// exchange of maxima costs what it saves (0.97 us); 128-key score tiles (0.97 us); q in shared memory, read again
+// for every unit (0.03 us more).  Two row tiles that share a unit's conversion took 11 % less per row than one did
+// then, but need twice the rows.  Tiles cut by their work, so that each SM has as many units, with parts joined by
+// the last CTA to arrive: a second tile per CTA and the joining cost 19 us, more than the even load gave (the four
+// prompts 104 us, 16 trees 89 us).
 //
 // Scales: the unit's K exponent (the largest of its pages'; codes of a page with a
 // smaller one are multiplied by the difference as they are converted, exact to
@@ -188,7 +191,8 @@ __device__ __forceinline__ float add_half(float c, uint16_t a) {
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_kv8_attention_args a, TcPlan pl) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (to a 1024-byte boundary by an offset, so that the compiler still knows what it points to as shared memory)
+  uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + M::bars);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + M::misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + M::misc + 4);
@@ -960,7 +964,8 @@ cudaError_t launch_kv8_tree(const Kv8View& c, const spec_kv8_attention_args& a, 
   const int units = (a.max_prefix + kKeys - 1) / kKeys;
   // A cluster shares a prefix only while SMs would idle, and a share is at least eight units: joining shares takes
   // 4 us, as long as five units (one tree of 61 nodes, 2048 tokens, 16 tiles: 32 us with one CTA each, 26, 20 and 21
-  // with 2, 4 and 6; 256 tiles of 512 - 4096 tokens: 83 us with one, 95 with two)
+  // with 2, 4 and 6; 192 tiles of 512 - 4096 tokens: 83 us with one, 95 with two).  More tiles than SMs start with the
+  // longest (16 trees, 192 tiles of 630 - 4096 tokens: 78 us, 82 in the batch's order)
   long long chunks = tiles > sm_count ? 1 : sm_count / tiles;
   chunks = chunks < units / 8 ? chunks : units / 8;
   chunks = chunks < 1 ? 1 : chunks > kKv8TcMaxChunks ? kKv8TcMaxChunks : chunks;
