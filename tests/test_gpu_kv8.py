@@ -386,6 +386,31 @@ def test_attention_nan_page_reaches_its_sequence_and_head_only(plane, nodes):
     check_attention(c, (got[0][:n, :2], got[1][:n, :2]), [x[:n, :2] for x in ref])
 
 
+@pytest.mark.parametrize("B,hkv", [(20, 8), (128, 2), (130, 2)])
+def test_attention_of_more_row_tiles_than_sms(B, hkv):
+    """Ragged batches whose tiles are started by length (up to 128 entries) or in order; equal lengths, no rows and no
+    prefix among them; one entry out of range and one whose length is above max_prefix stay as they were."""
+    g = np.random.default_rng(18)
+    prefixes = [int(x) for x in g.choice([0, 1, 30, 64, 65, 130], B)]
+    prefixes[7] = 131
+    nodes = [int(x) for x in g.choice([0, 9, 17, 20], B)]
+    nodes[3], nodes[7], nodes[9] = 20, 9, 17
+    c = attention_case(19, prefixes, nodes, 2 * hkv, hkv, 32, "bf16")
+    ref = reference(c)
+    ids = c["ids"].copy()
+    ids[9] = -1
+    T, o = sum(nodes), c["offsets"]
+    out = torch.full((T, 2 * hkv, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, 2 * hkv), 7.0, device="cuda")
+    run_attention(c, seq_ids=i32(ids), out=out, lse=lse, max_prefix=130)
+    left = np.zeros(T, bool)
+    for b in (7, 9):
+        left[o[b]:o[b + 1]] = True
+    rest = torch.from_numpy(~left).cuda()
+    assert (out[~rest] == 7).all() and (lse[~rest] == 7).all()
+    check_attention(c, (out[rest], lse[rest]), [x[~left] for x in ref])
+
+
 def test_refusals_of_the_torch_side():
     c = attention_case(17, [40], [2], 4, 2, 16, "bf16")
     cache, q = c["cache"], c["q"].cuda()
