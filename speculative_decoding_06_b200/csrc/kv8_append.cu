@@ -10,6 +10,14 @@
 // saturated to 448: half a step of e4m3, at most 2^-4 of a value.  A NaN makes its
 // page's exponent byte 255, which reads as NaN and stays until the page is opened
 // anew (place 0): the codes themselves need no NaN, and their readers no test.
+//
+// Prompts read and write each byte once: 195 MB of bf16 rows and their codes take 40 us, 4.9 TB/s, three quarters of the
+// measured copy rate.  A page's rows wait in registers for its largest value, so that the reads in flight are what four
+// CTAs of 256 threads per SM hold (three: 63 us before the instructions were cut; shared memory in place of registers,
+// six CTAs: 43 where registers took 42); issue slots are busy two thirds of the time, for the magnitudes, the products
+// and the conversions.  Tried without gain: heads of a row side by side in the grid, prefetch into L2 while the slots
+// are read, loads that bypass L1, CTAs of 512 threads (51 us).  Steps of a few rows are bound by the chain of loads:
+// slots, rows and the page's exponent, codes before the run where it grows (64 rows: 3.3 us; 317 gathered rows of 64 sequences in fp32: 6.1 us).
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -58,8 +66,7 @@ struct Top {
   }
   static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
     using T2 = std::conditional_t<__is_same(T, __half), __half2, __nv_bfloat162>;
-    a &= 0x7fff7fffu, b &= 0x7fff7fffu;
-    const T2 c = __hmax2_nan(reinterpret_cast<const T2&>(a), reinterpret_cast<const T2&>(b));
+    const T2 c = __hmax2_nan(__habs2(reinterpret_cast<const T2&>(a)), __habs2(reinterpret_cast<const T2&>(b)));
     return reinterpret_cast<const uint32_t&>(c);
   }
   __device__ __forceinline__ uint32_t bits() const { return max(m & 0x7fffu, m >> 16 & 0x7fffu); }
@@ -82,16 +89,37 @@ struct Top<float> {
   static __device__ __forceinline__ float value(uint32_t b) { return __uint_as_float(b); }
 };
 
-// eight values times `s` as e4m3, round to nearest even, saturating
-__device__ __forceinline__ uint2 encode8(const float* v, float s) {
-  uint32_t w[4];
+// four values as e4m3, round to nearest even, saturating
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+  uint32_t w;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(w)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return w;
+}
+// eight values times s, a power of two of 2^-120 .. 2^60, as e4m3
+template <typename T>
+__device__ __forceinline__ uint2 encode8(const Eight<T>& x, float s) {
+  float v[8];
+  if constexpr (__is_same(T, __nv_bfloat16)) {
+    // (both factors are bf16, the product is rounded once, to 32 bits: one instruction instead of two)
+    const uint16_t h = (uint16_t)(__float_as_uint(s) >> 16);
+    const uint32_t w[4] = {x.w[0].x, x.w[0].y, x.w[0].z, x.w[0].w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float2 y;
-    f2_unpack(f2_mul(f2_pack(v[2 * i], v[2 * i + 1]), f2_pack(s, s)), y.x, y.y);
-    w[i] = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+    for (int i = 0; i < 4; ++i) {
+      asm("fma.rn.f32.bf16 %0, %1, %2, %3;" : "=f"(v[2 * i]) : "h"((uint16_t)w[i]), "h"(h), "f"(-0.f));
+      asm("fma.rn.f32.bf16 %0, %1, %2, %3;" : "=f"(v[2 * i + 1]) : "h"((uint16_t)(w[i] >> 16)), "h"(h), "f"(-0.f));
+    }
+  } else {
+    x.get(v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      f2_unpack(f2_mul(f2_pack(v[2 * i], v[2 * i + 1]), f2_pack(s, s)), v[2 * i], v[2 * i + 1]);
   }
-  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+  return make_uint2(encode4(v[0], v[1], v[2], v[3]), encode4(v[4], v[5], v[6], v[7]));
 }
 
 // THREADS: half of them for K, half for V.  HELD rows per thread stay in registers, so that runs of
@@ -220,18 +248,14 @@ __global__ void __launch_bounds__(THREADS, CTAS) kv8_append_kernel(Kv8View c, sp
           const __nv_fp8_e4m3* h = reinterpret_cast<const __nv_fp8_e4m3*>(&was);
           float v[8];
 #pragma unroll
-          for (int q = 0; q < 8; ++q) v[q] = (float)h[q];
-          *p = encode8(v, f);
+          for (int q = 0; q < 8; ++q) v[q] = (float)h[q] * f;
+          *p = make_uint2(encode4(v[0], v[1], v[2], v[3]), encode4(v[4], v[5], v[6], v[7]));
         }
       }
     }
     const float f = pow2f(-e);
     uint8_t* const to = base + (size_t)place * kKv8Hd;
-    auto put = [&](int r, const Eight<T>& x) {
-      float v[8];
-      x.get(v);
-      *reinterpret_cast<uint2*>(to + (size_t)r * kKv8Hd) = encode8(v, f);
-    };
+    auto put = [&](int r, const Eight<T>& x) { *reinterpret_cast<uint2*>(to + r * kKv8Hd) = encode8(x, f); };
     for (int r = 0; r < n; r += kBatch) {
       if (n > kBatch) load(r);  // (a run of one batch is still there)
 #pragma unroll
@@ -256,7 +280,7 @@ void launch_append(const Kv8View& c, const spec_kv8_append_args& a, int per, cud
 cudaError_t launch_kv8_append(const Kv8View& c, const spec_kv8_append_args& a, int sm_count, cudaStream_t s) {
   // A sixteenth of an SM's share of the rows per CTA, at most a page: a CTA's runs are stored one after the other.
   // Up to four rows (decoding steps, accepted rows) CTAs have 128 threads (64 rows of bf16 and 8 heads: 3.3 us; 5.3
-  // with 256 threads), for prompts 256 (32k such rows, 195 MB: 42 us, 4.6 TB/s; 84 with 128).
+  // with 256 threads), for prompts 256 (31.7k such rows, 195 MB: 40 us, 4.9 TB/s; 84 with 128).
   int per = (int)((long long)a.rows * c.hkv / (16 * sm_count));
   per = per < 1 ? 1 : per > c.page ? c.page : per;
   if (a.dtype == SPEC_DTYPE_F32) launch_append<float>(c, a, per, s);
