@@ -1,7 +1,7 @@
 // Python binding of the spec_kv8_* calls over torch tensors: argument checks and
 // marshalling only.  A step's calls last a few microseconds on the GPU; checking a
 // dozen tensors through the ctypes binding took 15-19 us per call on the host, here
-// it takes about two.
+// 4-6 with the launch.
 #include <Python.h>
 
 #include <ATen/ATen.h>
