@@ -69,10 +69,11 @@ constexpr int kStages = 4;    // most operand stages of K or V
 constexpr int kByLength = 128;  // most sequences that are put in order
 constexpr int kScores = 3;    // S buffers: unit u has buffer u % 3
 
-// mbarriers: per operand stage; S, P and P V per S buffer; P V also per stream
+// mbarriers: per operand stage; S, P and P V per stream, for its even and its odd units: no wait is for a phase that
+// lies more than one behind what its waiter has seen, however far idle warps of a stream run ahead
 enum { B_Q = 0, B_O = 1, B_TREF = 2, B_DRAIN = 4, B_KFULL = 6, B_KEMPTY = B_KFULL + kStages, B_VFULL = B_KEMPTY + kStages,
-       B_VEMPTY = B_VFULL + kStages, B_SFULL = B_VEMPTY + kStages, B_PFULL = B_SFULL + kScores, B_PV = B_PFULL + kScores,
-       B_OUT = B_PV + kScores, B_CFULL = B_OUT + 2, B_CEMPTY = B_CFULL + 2 * kCodeStages, kNumBars = B_CEMPTY + 2 * kCodeStages };
+       B_VEMPTY = B_VFULL + kStages, B_SFULL = B_VEMPTY + kStages, B_PFULL = B_SFULL + 4, B_PV = B_PFULL + 4,
+       B_CFULL = B_PV + 4, B_CEMPTY = B_CFULL + 2 * kCodeStages, kNumBars = B_CEMPTY + 2 * kCodeStages };
 
 struct M {  // shared memory
   static constexpr int nk = 3;             // operand stages (units) of K
@@ -298,12 +299,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
       mbar_init(&bar[B_CFULL + s], 1);
       mbar_init(&bar[B_CEMPTY + s], kConvWarps);
     }
-    for (int s = 0; s < kScores; ++s) {
+    for (int s = 0; s < 4; ++s) {
       mbar_init(&bar[B_SFULL + s], 1);
       mbar_init(&bar[B_PFULL + s], 4);
       mbar_init(&bar[B_PV + s], 1);
     }
-    for (int s = 0; s < 2; ++s) mbar_init(&bar[B_OUT + s], 1);
     for (int s = 0; s < 2; ++s) mbar_init(&bar[B_TREF + s], 2 * kConvWarps);
     mbar_init(&bar[B_O], 2);
     mbar_init(&bar[B_DRAIN], 1);
@@ -361,36 +361,36 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
       const uint64_t dv = sw128_mnmajor_desc(smem_u32(smem + M::v), kHalf);
       const int n_own = (nu - t + 1) >> 1;  // units t, t + 2, ...
       int ks_ = t, kp = 0, vs = t, vp = 0;  // operand stages of K and V, and their phases
-      int sb = t, sp = 0, pb = t, pp = 0;   // S buffer of the next scores and of the next product, and their phases
+      int sb = t, pb = t;                   // S buffer of the next scores and of the next product
       bool ok = held(B_Q, 0);
       for (int i = 0; i <= n_own && ok; ++i) {
         if (i < n_own) {
-          // the S buffer holds P of three units ago until that one's product is done
-          ok = held(B_PV + sb, sp ^ 1) && held(B_KFULL + ks_, kp);
+          // the S buffer holds P of three units ago, unit j of the other stream, until that one's product is done
+          const int j = i - 2 + t;
+          ok = (j < 0 || held(B_PV + 2 * (t ^ 1) + (j & 1), (j >> 1) & 1)) && held(B_KFULL + ks_, kp);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)  // 16 dimensions per step: 8 columns of q (a descriptor's low bits count 16 bytes)
             tc_mma_ts(tmem + kColS + kKeys * sb, tmem + kColQ + 8 * ks,
                       dk + ((ks_ * kUnit + (ks >> 2) * kHalf + (ks & 3) * 32) >> 4), kIdescS, ks > 0 ? 1u : 0u);
-          tc_commit(&bar[B_SFULL + sb]);
+          tc_commit(&bar[B_SFULL + 2 * t + (i & 1)]);
           tc_commit(&bar[B_KEMPTY + ks_]);
           if ((ks_ += 2) >= M::nk) ks_ -= M::nk, kp ^= 1;
-          if ((sb += 2) >= kScores) sb -= kScores, sp ^= 1;
+          if ((sb += 2) >= kScores) sb -= kScores;
         }
         if (i > 0) {  // O += P V of the unit before
-          ok = held(B_VFULL + vs, vp) && held(B_PFULL + pb, pp);
+          ok = held(B_VFULL + vs, vp) && held(B_PFULL + 2 * t + ((i - 1) & 1), ((i - 1) >> 1) & 1);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)  // 16 keys per step: 8 columns of P
             tc_mma_ts(tmem + 128 * t, tmem + kColS + kKeys * pb + kk * 8, dv + ((vs * kUnit + kk * 16 * 128) >> 4),
                       kIdescPV, (i > 1 || kk > 0) ? 1u : 0u);
-          tc_commit(&bar[B_PV + pb]);
-          tc_commit(&bar[B_OUT + t]);
+          tc_commit(&bar[B_PV + 2 * t + ((i - 1) & 1)]);
           tc_commit(&bar[B_VEMPTY + vs]);
           if ((vs += 2) >= M::nv) vs -= M::nv, vp ^= 1;
-          if ((pb += 2) >= kScores) pb -= kScores, pp ^= 1;
+          if ((pb += 2) >= kScores) pb -= kScores;
         }
       }
       if (ok) {
@@ -658,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
     const float qs = s_row[r];
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);  // this warp's lanes
     const uint32_t to = tl + 128 * t;                                 // the stream's O
-    int sb = t, sp = 0;                                               // the unit's S buffer, its phase
+    int sb = t;                                                       // the unit's S buffer
     const int n_own = (nu - t + 1) >> 1;  // the stream's units
     float m = -INFINITY, l = 0.f, lr = 0.f;  // lr: of the rounded probabilities
     bool ok = true;
@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
       const float2 e = s_unit[u];
       const float f = qs * e.x, ve = e.y;
       const float un = fast_exp2(-ve);
-      if (ok) ok = held(B_SFULL + sb, sp);
+      if (ok) ok = held(B_SFULL + 2 * t + (i & 1), (i >> 1) & 1);
       ok = __all_sync(0xffffffffu, ok);
       if (ok && warp_on) {
         tc_fence_after();
@@ -719,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
           lr *= keep;
           if (i > 0) {
             // O shrinks: the product of the stream's last unit has to be in it
-            ok = __all_sync(0xffffffffu, held(B_OUT + t, (i - 1) & 1));
+            ok = __all_sync(0xffffffffu, held(B_PV + 2 * t + ((i - 1) & 1), ((i - 1) >> 1) & 1));
             if (ok) {
               tc_fence_after();
 #pragma unroll 1
@@ -765,8 +765,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
         tc_fence_before();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar[B_PFULL + sb]);
-      if ((sb += 2) >= kScores) sb -= kScores, sp ^= 1;
+      if (lane == 0) mbar_arrive(&bar[B_PFULL + 2 * t + (i & 1)]);
+      if ((sb += 2) >= kScores) sb -= kScores;
     }
     if (ok && nu > 0) ok = held(B_O, 0);
     ok = __all_sync(0xffffffffu, ok);

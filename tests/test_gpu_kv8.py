@@ -411,6 +411,23 @@ def test_attention_of_more_row_tiles_than_sms(B, hkv):
     check_attention(c, (out[rest], lse[rest]), [x[~left] for x in ref])
 
 
+@pytest.mark.parametrize("nodes,prefix,dtype", [(17, 100, "fp16"), (34, 700, "bf16"), (9, 260, "bf16")])
+def test_attention_with_idle_warps_repeats(nodes, prefix, dtype):
+    """Tiles whose last rows are empty, so that some warps have nothing to do between the barriers: 300 calls in a row
+    give the first one's results, which are right."""
+    c = attention_case(20, [prefix] * 40, [nodes] * 40, 8, 2, 64, dtype)
+    T = 40 * nodes
+    first = run_attention(c)
+    check_attention(c, first, reference(c))
+    out, lse = torch.empty_like(first[0]), torch.empty(T, 8, device="cuda")
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    ws = c["cache"].attention_workspace(40, 8, c["nodes"], c["prefix"])
+    for _ in range(300):
+        run_attention(c, out=out, lse=lse, workspace=ws)
+        wrong += (out != first[0]).any() | (lse != first[1]).any()
+    assert int(wrong) == 0
+
+
 def test_refusals_of_the_torch_side():
     c = attention_case(17, [40], [2], 4, 2, 16, "bf16")
     cache, q = c["cache"], c["q"].cuda()
