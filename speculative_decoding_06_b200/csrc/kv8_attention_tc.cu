@@ -53,8 +53,6 @@ constexpr int kKeys = 64;  // keys of a unit
 constexpr int kConvWarps = 4;  // per plane
 constexpr int kConvThreads = 32 * kConvWarps;
 constexpr int kCodeStages = 3;
-constexpr uint32_t kQHalf = kRowTile * 128;  // [128 rows][64 fp16]: 16 KB
-constexpr uint32_t kQTile = 2 * kQHalf;
 constexpr uint32_t kHalf = kKeys * 128;      // [64 keys][64 fp16]: 8 KB
 constexpr uint32_t kUnit = 2 * kHalf;        // one unit's K or V
 constexpr uint32_t kCodeTile = kKeys * kKv8Hd;  // one plane
@@ -63,7 +61,8 @@ constexpr int kMaxUnits = kKv8TcMaxKeys / kKeys;  // of a CTA's share: their pag
 constexpr int kRowWarps = 8;  // two streams of four
 constexpr int kIssueWarp = kRowWarps + 2 * kConvWarps;  // and the next one: one per stream
 constexpr int kLoadWarp = kIssueWarp + 2;
-constexpr int kThreads = 32 * (kLoadWarp + 1);
+constexpr int kHelpWarp = kLoadWarp + 1;  // ancestors
+constexpr int kThreads = 32 * (kHelpWarp + 1);
 constexpr int kStages = 4;    // most operand stages of K or V
 
 constexpr int kByLength = 128;  // most sequences that are put in order
@@ -71,15 +70,19 @@ constexpr int kScores = 3;    // S buffers: unit u has buffer u % 3
 
 // mbarriers: per operand stage; S, P and P V per stream, for its even and its odd units: no wait is for a phase that
 // lies more than one behind what its waiter has seen, however far idle warps of a stream run ahead
-enum { B_Q = 0, B_O = 1, B_TREF = 2, B_DRAIN = 4, B_KFULL = 6, B_KEMPTY = B_KFULL + kStages, B_VFULL = B_KEMPTY + kStages,
+enum { B_Q = 0, B_O = 1, B_TREF = 2, B_DRAIN = 4, B_ANC = 6, B_KFULL = 7, B_KEMPTY = B_KFULL + kStages, B_VFULL = B_KEMPTY + kStages,
        B_VEMPTY = B_VFULL + kStages, B_SFULL = B_VEMPTY + kStages, B_PFULL = B_SFULL + 4, B_PV = B_PFULL + 4,
        B_CFULL = B_PV + 4, B_CEMPTY = B_CFULL + 2 * kCodeStages, kNumBars = B_CEMPTY + 2 * kCodeStages };
+
+constexpr uint32_t kJoin = kRowTile * (512 + 2 * 256);
+
+constexpr uint32_t kQPitch = kKv8Hd * 2 + 16;  // a row of q: its pieces of 16 bytes meet in no bank
 
 struct M {  // shared memory
   static constexpr int nk = 3;             // operand stages (units) of K
   static constexpr int nv = 4;             // and V
   static constexpr uint32_t q = 0;
-  static constexpr uint32_t k = q + kQTile;
+  static constexpr uint32_t k = q + (kRowTile * kQPitch + 1023) / 1024 * 1024;
   static constexpr uint32_t v = k + nk * kUnit;
   static constexpr uint32_t codes = v + nv * kUnit;
   static constexpr uint32_t group = codes + 2 * kCodeStages * kCodeTile;  // int4 [kMaxUnits]: first rows / 16 of the groups of 16 keys
@@ -88,17 +91,19 @@ struct M {  // shared memory
   static constexpr uint32_t unit = vexp + 4 * kMaxUnits;  // float2 [kMaxUnits + 2]: factor of K, exponent of V
   static constexpr uint32_t anc = unit + 8 * (kMaxUnits + 2);  // uint64 [2][128][2]
   static constexpr uint32_t jump = anc + 2 * 128 * 16;    // int [2][128]
-  static constexpr uint32_t row = jump + 2 * 128 * 4;     // float [2][128]: q's factor, at the end the log-sum-exp
+  static constexpr uint32_t half = jump + 2 * 128 * 4;    // float [2][128]: largest values of the halves of q, at the end the streams' log-sum-exps
+  static constexpr uint32_t row = half + 2 * 128 * 4;     // float [256]: at the end the rows' log-sum-exps
   static constexpr uint32_t red = row + 2 * 128 * 4;      // float [8]: the converter warps' largest K and V values
   static constexpr uint32_t vbad = red + 32;              // uint32 [4]: own rows whose V holds an infinity or NaN
   static constexpr uint32_t bars = vbad + 16;
   static constexpr uint32_t misc = bars + 8 * kNumBars + 8;
   static constexpr uint32_t end = misc + 16;
   static constexpr uint32_t dyn = end + 1024;             // to a 1024-byte boundary
-  static constexpr uint32_t stage = q;                    // O, 128 rows x 512 B per stream, over the operands
+  // at the end, over the operands: the tile's O (128 rows of 512 B), then half a row of each stream for the other
+  static constexpr uint32_t stage = 0;
 };
 static_assert(M::dyn <= 227 * 1024, "shared memory");
-static_assert(M::codes - M::stage >= 2 * 128 * 512, "staging");
+static_assert(M::codes - M::stage >= kJoin, "staging");
 
 // TMEM columns: O of the streams, the S buffers (P lies over the first half of its S), q as the scores' A operand.
 // (q in shared memory would be read again for every unit: 256 of the 1024 cycles that a unit then takes of the
@@ -139,7 +144,6 @@ __device__ __forceinline__ float exp_of(int byte) { return byte >= 255 ? NAN : (
 __device__ __forceinline__ int max4(uint32_t w) {
   return max(max((int)(w & 255), (int)(w >> 8 & 255)), max((int)(w >> 16 & 255), (int)(w >> 24)));
 }
-__device__ __forceinline__ float finite_or_0(float x) { return fabsf(x) < INFINITY ? x : 0.f; }
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -169,6 +173,13 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8], float f) {
 // largest magnitude of two 16-bit values' bits (sign cleared), pairwise
 __device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7fff7fffu); }
 template <typename T> __device__ __forceinline__ constexpr uint32_t inf_bits() { return __is_same(T, __half) ? 0x7c00u : 0x7f80u; }
+// the same by the type's own maximum, NaN above all others
+template <typename T>
+__device__ __forceinline__ uint32_t max_abs_nan(uint32_t m, uint32_t w) {
+  using T2 = std::conditional_t<__is_same(T, __half), __half2, __nv_bfloat162>;
+  const T2 y = __hmax2_nan(reinterpret_cast<const T2&>(m), __habs2(reinterpret_cast<const T2&>(w)));
+  return reinterpret_cast<const uint32_t&>(y);
+}
 // sets infinities and NaN among eight 16-bit values to 0; whether there were any
 template <typename T>
 __device__ __forceinline__ bool finite_only(uint4& r) {
@@ -203,6 +214,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
   float* s_row = reinterpret_cast<float*>(smem + M::row);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (warp == kLoadWarp && lane == 0) {
+    mbar_init(&bar[B_Q], kRowWarps);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&bar[B_KFULL + s], kConvWarps);
+      mbar_init(&bar[B_KEMPTY + s], 1);
+      mbar_init(&bar[B_VFULL + s], kConvWarps);
+      mbar_init(&bar[B_VEMPTY + s], 1);
+    }
+    for (int s = 0; s < 2 * kCodeStages; ++s) {
+      mbar_init(&bar[B_CFULL + s], 1);
+      mbar_init(&bar[B_CEMPTY + s], kConvWarps);
+    }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&bar[B_SFULL + s], 1);
+      mbar_init(&bar[B_PFULL + s], 4);
+      mbar_init(&bar[B_PV + s], 1);
+    }
+    for (int s = 0; s < 2; ++s) mbar_init(&bar[B_TREF + s], 2 * kConvWarps);
+    mbar_init(&bar[B_O], 2);
+    mbar_init(&bar[B_DRAIN], 1);
+    mbar_init(&bar[B_DRAIN + 1], 1);
+    mbar_init(&bar[B_ANC], 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
   const int G = a.n_q_heads / c.hkv;
   auto by_g = [&](int x) { return (int)((uint32_t)x * pl.by_group >> 20); };
   // grid: x = row tiles * chunks (a cluster is the chunks of a row tile), y = kv heads, z = batch.  The CTAs of a
@@ -233,83 +269,99 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
   const int P = a.lengths[seq];
   const int rows = n * G;
   if (P < 0 || P > a.max_prefix || row0 >= rows) return;
-  // this CTA's share of the prefix, whole tiles; the last one also has the step's own rows
-  const int per = pl.chunks == 1 ? P : ((int)__umulhi((uint32_t)(P + pl.chunks - 1), pl.by_chunks) + kKeys - 1) / kKeys * kKeys;
+  // this CTA's share of the prefix, whole units; the last one also has the step's own rows, which take as long as two
+  const int even = (int)__umulhi((uint32_t)(P + (a.k_new ? 2 * kKeys : 0) + pl.chunks - 1), pl.by_chunks);
+  const int per = pl.chunks == 1 ? P : min((even + kKeys - 1) / kKeys * kKeys, kKv8TcMaxKeys);
   const int c0 = min(P, share * per), c1 = min(P, c0 + per);
   const int top = min(n - 1, by_g(row0 + kRowTile - 1));  // last node that a row here can see
   const int np = (c1 - c0 + kKeys - 1) / kKeys;                   // units of the prefix
   const int nt = (a.k_new && share == pl.chunks - 1) ? top / kKeys + 1 : 0;  // of the step's own rows: they come last
   const int nu = np + nt;
 
-  // q: half a warp per row, 16 rows per warp and tile, the first tile's on their way while the pages are looked up
-  uint4 qraw[8];
-  int parent = -1;
-  auto load_q = [&](int tile) {
+  // the copies of the first units start before the CTA's other threads are ready for them
+  const uint32_t ring = smem_u32(smem + M::codes);
+  auto load_unit = [&](int u, int st, int p) {
+    const int4 at = s_group[u];
+    uint64_t* full = &bar[B_CFULL + p * kCodeStages + st];
+    mbar_arrive_expect_tx(full, kCodeTile);
+    const uint32_t dst = ring + (p * kCodeStages + st) * kCodeTile;
+    const uint8_t* src = c.codes[p];
+    if (at.y == at.x + 1 && at.z == at.x + 2 && at.w == at.x + 3) {  // one stretch of memory
+      bulk_load(dst, src + (size_t)at.x * (16 * kKv8Hd), kCodeTile, full);
+    } else {
+      bulk_load(dst, src + (size_t)at.x * (16 * kKv8Hd), kCodeTile / 4, full);
+      bulk_load(dst + kCodeTile / 4, src + (size_t)at.y * (16 * kKv8Hd), kCodeTile / 4, full);
+      bulk_load(dst + kCodeTile / 2, src + (size_t)at.z * (16 * kKv8Hd), kCodeTile / 4, full);
+      bulk_load(dst + kCodeTile / 4 * 3, src + (size_t)at.w * (16 * kKv8Hd), kCodeTile / 4, full);
+    }
+  };
+  ulonglong2* const s_anc = reinterpret_cast<ulonglong2*>(smem + M::anc);
+  int* const s_jump = reinterpret_cast<int*>(smem + M::jump);
+  uint4 qraw[8];  // half a warp per row, 16 rows per row warp
+  if (warp < kRowWarps) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int qr = row0 + kRowTile * tile + 16 * warp + 2 * i + (lane >> 4);
-      const int node = by_g(qr);
+      const int qr = row0 + 16 * warp + 2 * i + (lane >> 4), node = by_g(qr);
       qraw[i] = make_uint4(0, 0, 0, 0);
       if (qr < rows)
         qraw[i] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q) + a.q_row_stride * (first + node) +
                                                        a.q_head_stride * (kvh * G + (qr - node * G))) + (lane & 15));
     }
-  };
-  if (warp < kRowWarps) {
-    load_q(0);
-    if (nt > 0 && a.parents && tid <= top) parent = a.parents[first + tid];
+  } else if (warp == kHelpWarp) {
+    if (nt > 0 && a.parents) {
+      for (int node = lane; node < 128; node += 32) {
+        const int up = node <= top ? a.parents[first + node] : -1;
+        s_anc[node] = make_ulonglong2(node < 64 ? 1ull << node : 0ull, node < 64 ? 0ull : 1ull << (node - 64));
+        s_jump[node] = up < node && up >= 0 ? up : -1;
+      }
+    }
   } else {
-    // pages of the share's units: four groups of 16 keys, each inside one page
-    for (int i = tid - 32 * kRowWarps; i < np; i += kThreads - 32 * kRowWarps) {
+    // pages of the share's units: four groups of 16 keys, each inside one page; the loading warp has the first ones
+    for (int i0 = warp == kLoadWarp ? 0 : 32 * (warp - kRowWarps + 1); i0 < np; i0 += 32 * (kHelpWarp - kRowWarps)) {
+      const int i = i0 + lane;
       int pg[4], at[4];
-      uint32_t ke = 0, ve = 0;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int key = c0 + kKeys * i + 16 * u;
-        pg[u] = key < c1 ? a.tables[(size_t)seq * a.max_blocks + (key >> c.page_log2)] : -2;
+        pg[u] = key < c1 ? a.tables[(size_t)seq * a.max_blocks + (key >> c.page_log2)] : -1;
       }
+      uint32_t bad = 0;  // keys without a page
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const bool none = pg[u] == -2, ok = pg[u] >= 0 && pg[u] < c.n_pages;
-        if (!ok) pg[u] = 0;
-        at[u] = pg[u] * c.hkv + kvh;
-        ke |= (none ? 0u : !ok && c0 + kKeys * i + 16 * u < c1 ? 255u : (uint32_t)c.exps[0][at[u]]) << (8 * u);
-        ve |= (none ? 0u : (uint32_t)c.exps[1][at[u]]) << (8 * u);
-        at[u] = ((at[u] << c.page_log2) + ((c0 + kKeys * i + 16 * u) & (c.page - 1))) >> 4;
+        const bool ok = pg[u] >= 0 && pg[u] < c.n_pages;
+        if (!ok && c0 + kKeys * i + 16 * u < c1) bad |= 255u << (8 * u);
+        at[u] = (ok ? pg[u] : 0) * c.hkv + kvh;
       }
-      s_group[i] = make_int4(at[0], at[1], at[2], at[3]);
-      reinterpret_cast<uint32_t*>(smem + M::kexp)[i] = ke;
-      reinterpret_cast<uint32_t*>(smem + M::vexp)[i] = ve;
-      s_unit[i] = make_float2(scale_of(max4(ke)), exp_of(max4(ve)));
+      if (i < np) {
+        int w[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) w[u] = ((at[u] << c.page_log2) + ((c0 + kKeys * i + 16 * u) & (c.page - 1))) >> 4;
+        s_group[i] = make_int4(w[0], w[1], w[2], w[3]);
+      }
+      if (warp == kLoadWarp && i0 == 0) {
+        __syncwarp();
+        if (elect_one())
+          for (int u = 0; u < min(np, kCodeStages); ++u)
+            for (int p = 0; p < 2; ++p) load_unit(u, u, p);
+        __syncwarp();
+      }
+      if (i < np) {
+        uint32_t ke = bad, ve = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const bool none = c0 + kKeys * i + 16 * u >= c1;
+          ke |= (none ? 0u : (uint32_t)c.exps[0][at[u]]) << (8 * u);
+          ve |= (none ? 0u : (uint32_t)c.exps[1][at[u]]) << (8 * u);
+        }
+        reinterpret_cast<uint32_t*>(smem + M::kexp)[i] = ke;
+        reinterpret_cast<uint32_t*>(smem + M::vexp)[i] = ve;
+        s_unit[i] = make_float2(scale_of(max4(ke)), exp_of(max4(ve)));
+      }
     }
   }
   if (warp == kIssueWarp) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
-  }
-  if (tid == 0) {
-    mbar_init(&bar[B_Q], kRowWarps);
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&bar[B_KFULL + s], kConvWarps);
-      mbar_init(&bar[B_KEMPTY + s], 1);
-      mbar_init(&bar[B_VFULL + s], kConvWarps);
-      mbar_init(&bar[B_VEMPTY + s], 1);
-    }
-    for (int s = 0; s < 2 * kCodeStages; ++s) {
-      mbar_init(&bar[B_CFULL + s], 1);
-      mbar_init(&bar[B_CEMPTY + s], kConvWarps);
-    }
-    for (int s = 0; s < 4; ++s) {
-      mbar_init(&bar[B_SFULL + s], 1);
-      mbar_init(&bar[B_PFULL + s], 4);
-      mbar_init(&bar[B_PV + s], 1);
-    }
-    for (int s = 0; s < 2; ++s) mbar_init(&bar[B_TREF + s], 2 * kConvWarps);
-    mbar_init(&bar[B_O], 2);
-    mbar_init(&bar[B_DRAIN], 1);
-    mbar_init(&bar[B_DRAIN + 1], 1);
-    *abort_flag = 0;
-    fence_barrier_init();
   }
   if (tid < 4) s_vbad[tid] = 0u;
   tc_fence_before();
@@ -318,31 +370,40 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
   const uint32_t tmem = *tmem_slot;
   auto held = [&](int which, uint32_t parity) { return mbar_wait(&bar[which], parity, nullptr, abort_flag); };
 
-  if (warp == kLoadWarp) {
+  if (warp == kHelpWarp) {
+    // ------------------------------------------------------------ ancestors: each node's set doubles its reach per round
+    if (nt > 0 && a.parents) {
+      __syncwarp();
+      int cur = 0;
+      for (int reach = 1; reach <= top; reach *= 2) {
+#pragma unroll
+        for (int node = lane; node < 128; node += 32) {
+          ulonglong2 set = s_anc[128 * cur + node];
+          int up = s_jump[128 * cur + node];
+          if (up >= 0) {
+            const ulonglong2 more = s_anc[128 * cur + up];
+            set.x |= more.x;
+            set.y |= more.y;
+            up = s_jump[128 * cur + up];
+          }
+          s_anc[128 * (cur ^ 1) + node] = set;
+          s_jump[128 * (cur ^ 1) + node] = up;
+        }
+        cur ^= 1;
+        __syncwarp();
+      }
+      if (lane == 0) mbar_arrive(&bar[B_ANC]);
+    }
+  } else if (warp == kLoadWarp) {
     // ------------------------------------------------------------ loads
     if (elect_one()) {
-      const uint32_t ring = smem_u32(smem + M::codes);
       bool ok = true;
-      int st = 0, ph = 1, u = 0;
-      for (; u < np && ok; ++u) {
-        const int4 at = s_group[u];
+      int u = min(np, kCodeStages);
+      for (int st = 0, ph = 0; u < np && ok; ++u) {
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          const int sp = p * kCodeStages + st;
-          ok = ok && held(B_CEMPTY + sp, ph);
-          if (!ok) break;
-          uint64_t* full = &bar[B_CFULL + sp];
-          mbar_arrive_expect_tx(full, kCodeTile);
-          const uint32_t dst = ring + sp * kCodeTile;
-          const uint8_t* src = c.codes[p];
-          if (at.y == at.x + 1 && at.z == at.x + 2 && at.w == at.x + 3) {  // one stretch of memory
-            bulk_load(dst, src + (size_t)at.x * (16 * kKv8Hd), kCodeTile, full);
-          } else {
-            bulk_load(dst, src + (size_t)at.x * (16 * kKv8Hd), kCodeTile / 4, full);
-            bulk_load(dst + kCodeTile / 4, src + (size_t)at.y * (16 * kKv8Hd), kCodeTile / 4, full);
-            bulk_load(dst + kCodeTile / 2, src + (size_t)at.z * (16 * kKv8Hd), kCodeTile / 4, full);
-            bulk_load(dst + kCodeTile / 4 * 3, src + (size_t)at.w * (16 * kKv8Hd), kCodeTile / 4, full);
-          }
+          ok = ok && held(B_CEMPTY + p * kCodeStages + st, ph);
+          if (ok) load_unit(u, st, p);
         }
         if (++st == kCodeStages) st = 0, ph ^= 1;
       }
@@ -427,7 +488,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
       if (++st == n_stages) st = 0, ph ^= 1;
     };
     const uint32_t* const s_exp = reinterpret_cast<const uint32_t*>(smem + (p ? M::vexp : M::kexp));
-    // the step's own rows, 64 nodes per tile: their largest finite value sets the tile's exponent
+    // the step's own rows, 64 nodes per tile: their largest finite value sets the tile's exponent.  They are looked at
+    // last, while the prefix's last units wait for their turn
     const T* const own = reinterpret_cast<const T*>(p ? a.v_new : a.k_new) +
                          (p ? a.v_head_stride : a.k_head_stride) * kvh + 16 * ch;
     const int64_t own_stride = p ? a.v_row_stride : a.k_row_stride;
@@ -440,41 +502,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
         raw[1] = __ldg(at + 1);
       }
     };
-    for (int tt = 0; tt < nt; ++tt) {
-      uint4 raw[4][2];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) own_row(tt, u, raw[u]);
-      uint32_t big = 0;
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const uint4 r = raw[u >> 1][u & 1];
-        big = max_abs2(max_abs2(max_abs2(max_abs2(big, r.x), r.y), r.z), r.w);
-      }
-      if (max(big & 0xffffu, big >> 16) >= inf_bits<T>()) {  // (rare) infinities or NaN
-        big = 0;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          bool wild = false;
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) wild |= finite_only<T>(raw[u][hh]);
-          big = max_abs2(max_abs2(max_abs2(max_abs2(big, raw[u][0].x), raw[u][0].y), raw[u][0].z), raw[u][0].w);
-          big = max_abs2(max_abs2(max_abs2(max_abs2(big, raw[u][1].x), raw[u][1].y), raw[u][1].z), raw[u][1].w);
-          const int node = kKeys * tt + 16 * u + kr;
-          if (p && wild) atomicOr(&s_vbad[node >> 5], 1u << (node & 31));
-        }
-      }
-      big = __reduce_max_sync(0xffffffffu, max(big & 0xffffu, big >> 16));
-      uint32_t* red = reinterpret_cast<uint32_t*>(smem + M::red) + kConvWarps * p;
-      if (lane == 0) red[x >> 5] = big;
-      sync_converters(p);
-#pragma unroll
-      for (int w = 0; w < kConvWarps; ++w) big = max(big, red[w]);
-      const uint16_t top_bits = (uint16_t)big;
-      const int shift = shift_of(to_f32<T>(*reinterpret_cast<const T*>(&top_bits)));
-      if (x == 0) (&s_unit[np + tt].x)[p] = p ? (float)shift : pow2i(shift);
-      sync_converters(p);  // (also: everyone has read `red`)
-      if (lane == 0) mbar_arrive(&bar[B_TREF + tt]);
-    }
     const uint8_t* const codes = smem + M::codes + p * (kCodeStages * kCodeTile) + kr * kKv8Hd + 16 * ch;
     int cs = 0, cp = 0;  // stage of the codes, its phase
     for (int j = 0; j < np; ++j) {
@@ -525,6 +552,42 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
       if (lane == 0) mbar_arrive(&bar[B_CEMPTY + p * kCodeStages + cs]);  // (all lanes have read theirs: arrive() syncs)
       if (++cs == kCodeStages) cs = 0, cp ^= 1;
     }
+    // (whatever `ok`: the plane's warps meet here)
+    for (int tt = 0; tt < nt; ++tt) {
+      uint4 raw[4][2];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) own_row(tt, u, raw[u]);
+      uint32_t big = 0;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const uint4 r = raw[u >> 1][u & 1];
+        big = max_abs_nan<T>(max_abs_nan<T>(max_abs_nan<T>(max_abs_nan<T>(big, r.x), r.y), r.z), r.w);
+      }
+      if (max(big & 0xffffu, big >> 16) >= inf_bits<T>()) {  // (rare) infinities or NaN
+        big = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          bool wild = false;
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) wild |= finite_only<T>(raw[u][hh]);
+          big = max_abs2(max_abs2(max_abs2(max_abs2(big, raw[u][0].x), raw[u][0].y), raw[u][0].z), raw[u][0].w);
+          big = max_abs2(max_abs2(max_abs2(max_abs2(big, raw[u][1].x), raw[u][1].y), raw[u][1].z), raw[u][1].w);
+          const int node = kKeys * tt + 16 * u + kr;
+          if (p && wild) atomicOr(&s_vbad[node >> 5], 1u << (node & 31));
+        }
+      }
+      big = __reduce_max_sync(0xffffffffu, max(big & 0xffffu, big >> 16));
+      uint32_t* red = reinterpret_cast<uint32_t*>(smem + M::red) + kConvWarps * p;
+      if (lane == 0) red[x >> 5] = big;
+      sync_converters(p);
+#pragma unroll
+      for (int w = 0; w < kConvWarps; ++w) big = max(big, red[w]);
+      const uint16_t top_bits = (uint16_t)big;
+      const int shift = shift_of(to_f32<T>(*reinterpret_cast<const T*>(&top_bits)));
+      if (x == 0) (&s_unit[np + tt].x)[p] = p ? (float)shift : pow2i(shift);
+      sync_converters(p);  // (also: everyone has read `red`)
+      if (lane == 0) mbar_arrive(&bar[B_TREF + tt]);
+    }
     for (int tt = 0; tt < nt && ok; ++tt) {
       const int j = np + tt;
       uint8_t* const op = enter();
@@ -555,113 +618,67 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
     // ------------------------------------------------------------ softmax rows
     const int t = warp >> 2;                 // stream
     const int r = (warp & 3) * 32 + lane;    // TMEM lane
-    const int qr = row0 + r;
-    const bool row_ok = qr < rows;
-    const int node = row_ok ? by_g(qr) : 0;
-    const bool warp_on = __any_sync(0xffffffffu, row_ok);
-    // q as fp16: bf16 rows times a power of two (see shift_of)
-    int qex[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) qex[i] = 0;
-    if (!__is_same(T, __half)) {
-      float mq[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float v[8];
-        unpack8<T>(qraw[i], v);
-        mq[i] = fmaxf(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))),
-                      fmaxf(fmaxf(fabsf(v[4]), fabsf(v[5])), fmaxf(fabsf(v[6]), fabsf(v[7]))));  // (NaN is passed over)
+    const bool warp_on = __any_sync(0xffffffffu, row0 + r < rows);
+    // what the row sees of the step's own rows, in the last of the rounds' buffers
+    auto seen = [&](uint64_t& lo, uint64_t& hi) {
+      const int node = row0 + r < rows ? by_g(row0 + r) : 0;
+      if (a.parents) {
+        held(B_ANC, 0);
+        const ulonglong2 set = s_anc[128 * ((32 - __clz(top)) & 1) + node];
+        lo = set.x, hi = set.y;
+      } else {
+        lo = node >= 63 ? ~0ull : (2ull << node) - 1;
+        hi = node < 64 ? 0 : node >= 127 ? ~0ull : (2ull << (node - 64)) - 1;
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (mq[i] == INFINITY) {  // (rare) the largest of the finite values
-          mq[i] = 0.f;
-#pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t w = q == 0 ? qraw[i].x : q == 1 ? qraw[i].y : q == 2 ? qraw[i].z : qraw[i].w;
-            mq[i] = fmaxf(mq[i], fmaxf(fabsf(finite_or_0(__uint_as_float(w << 16))),
-                                       fabsf(finite_or_0(__uint_as_float(w & 0xffff0000u)))));
-          }
-        }
-      }
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mq[i] = fmaxf(mq[i], __shfl_xor_sync(0xffffffffu, mq[i], o));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) qex[i] = shift_of(mq[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int qrow = 16 * warp + 2 * i + (lane >> 4);
-      uint4 y = qraw[i];
-      if (!__is_same(T, __half)) {
-        float v[8];
-        unpack8<T>(y, v);
-        y = pack8(v, pow2i(-qex[i]));
-      }
-      *reinterpret_cast<uint4*>(smem + M::q + ((lane >> 3) & 1) * kQHalf + qrow * 128 + (((lane & 7) ^ (qrow & 7)) << 4)) = y;
-      if ((lane & 15) == 0) s_row[qrow] = a.scale * 1.4426950408889634f * pow2i(qex[i]);
-    }
-    // ancestors: each node's set doubles its reach per round (128 nodes: seven rounds)
-    uint64_t anc0 = 0, anc1 = 0;
+    };
+    // q as fp16 into tensor memory, half a row per thread: bf16 rows times a power of two (see shift_of), which the
+    // largest finite value of both halves sets
+    float* const s_half = reinterpret_cast<float*>(smem + M::half);
+    float qs = a.scale * 1.4426950408889634f;
+    bool ok = true;
     {
-      ulonglong2* set = reinterpret_cast<ulonglong2*>(smem + M::anc);
-      int* jump = reinterpret_cast<int*>(smem + M::jump);
-      if (nt > 0 && a.parents && tid < 128) {
-        set[tid] = make_ulonglong2(tid < 64 ? 1ull << tid : 0ull, tid < 64 ? 0ull : 1ull << (tid - 64));
-        jump[tid] = parent < tid && parent >= 0 ? parent : -1;
-      }
-      sync_rows();
-      {  // this thread's row of q, dimensions 64 t .., into tensor memory
-        uint32_t w[32];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint4 y = *reinterpret_cast<const uint4*>(smem + M::q + t * kQHalf + r * 128 + ((i ^ (r & 7)) << 4));
-          w[4 * i] = y.x, w[4 * i + 1] = y.y, w[4 * i + 2] = y.z, w[4 * i + 3] = y.w;
-        }
-        tmem_st32_async(tmem + ((uint32_t)((warp & 3) * 32) << 16) + kColQ + 32 * t, w);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[B_Q]);
+      for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<uint4*>(smem + M::q + (16 * warp + 2 * i + (lane >> 4)) * kQPitch + 16 * (lane & 15)) = qraw[i];
+      sync_rows();
+      uint32_t w[32];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint4 y = *reinterpret_cast<const uint4*>(smem + M::q + r * kQPitch + 128 * t + 16 * i);
+        w[4 * i] = y.x, w[4 * i + 1] = y.y, w[4 * i + 2] = y.z, w[4 * i + 3] = y.w;
       }
-      int cur = 0;
-      if (nt > 0 && a.parents) {
-        for (int reach = 1; reach <= top; reach *= 2) {
-          if (tid < 128) {
-            ulonglong2 s = set[cur * 128 + tid];
-            int up = jump[cur * 128 + tid];
-            if (up >= 0) {
-              const ulonglong2 s2 = set[cur * 128 + up];
-              s.x |= s2.x;
-              s.y |= s2.y;
-              up = jump[cur * 128 + up];
-            }
-            set[(cur ^ 1) * 128 + tid] = s;
-            jump[(cur ^ 1) * 128 + tid] = up;
+      if (!__is_same(T, __half)) {
+        uint32_t big = 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) big = max_abs_nan<T>(big, w[i]);
+        big = max(big & 0xffffu, big >> 16);
+        if (big >= inf_bits<T>()) {  // (rare) of the finite ones
+          big = 0;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const uint32_t lo = w[i] & 0x7fffu, hi = w[i] >> 16 & 0x7fffu;
+            big = max(big, max(lo < inf_bits<T>() ? lo : 0u, hi < inf_bits<T>() ? hi : 0u));
           }
-          cur ^= 1;
-          sync_rows();
         }
+        s_half[tid] = __uint_as_float(big << 16);
+        sync_rows();
+        const int shift = shift_of(fmaxf(s_half[tid], s_half[tid ^ 128]));
+        const float f = pow2i(-shift);
+        qs *= pow2i(shift);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) w[i] = pack2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
       }
-      if (nt > 0) {
-        if (a.parents) {
-          anc0 = set[cur * 128 + node].x;
-          anc1 = set[cur * 128 + node].y;
-        } else {
-          anc0 = node >= 63 ? ~0ull : (2ull << node) - 1;
-          anc1 = node < 64 ? 0 : node >= 127 ? ~0ull : (2ull << (node - 64)) - 1;
-        }
-      }
+      tmem_st32_async(tmem + ((uint32_t)((warp & 3) * 32) << 16) + kColQ + 32 * t, w);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[B_Q]);
     }
-    const float qs = s_row[r];
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);  // this warp's lanes
     const uint32_t to = tl + 128 * t;                                 // the stream's O
-    int sb = t;                                                       // the unit's S buffer
+    int sb = t, eo = 2 * t, ph = 0;                                   // the unit's S buffer, barrier and phase
     const int n_own = (nu - t + 1) >> 1;  // the stream's units
     float m = -INFINITY, l = 0.f, lr = 0.f;  // lr: of the rounded probabilities
-    bool ok = true;
 #pragma unroll 1
     for (int i = 0; i < n_own; ++i) {
       const int u = 2 * i + t;
@@ -670,7 +687,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
       if (u >= np - 1) {
         if (u >= np) {
           if (ok) ok = held(B_TREF + u - np, 0);
-          see = u == np ? anc0 : anc1;
+          uint64_t lo, hi;
+          seen(lo, hi);
+          see = u == np ? lo : hi;
         } else {
           const int left = c1 - (c0 + kKeys * u);
           if (left < kKeys) see = (1ull << left) - 1;
@@ -679,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
       const float2 e = s_unit[u];
       const float f = qs * e.x, ve = e.y;
       const float un = fast_exp2(-ve);
-      if (ok) ok = held(B_SFULL + 2 * t + (i & 1), (i >> 1) & 1);
+      if (ok) ok = held(B_SFULL + eo, ph);
       ok = __all_sync(0xffffffffu, ok);
       if (ok && warp_on) {
         tc_fence_after();
@@ -765,12 +784,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
         tc_fence_before();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar[B_PFULL + 2 * t + (i & 1)]);
+      if (lane == 0) mbar_arrive(&bar[B_PFULL + eo]);
+      ph ^= eo & 1;
+      eo ^= 1;
       if ((sb += 2) >= kScores) sb -= kScores;
     }
     if (ok && nu > 0) ok = held(B_O, 0);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) *abort_flag = 1;
+    int place = row0 + r;
+    asm volatile("" : "+r"(place));  // (computed here: a register less in the loop)
+    const int qr = place;
+    const bool row_ok = qr < rows;
+    const int node = row_ok ? by_g(qr) : 0;
     // normalised output of this stream; two streams of the same rows join in the first one.  It is written out, or
     // staged over operands that are done with (B_O follows every MMA) where a cluster shares the prefix.
     float inv = !ok ? NAN : l == 0.f ? 0.f : 1.f / lr;
@@ -778,8 +804,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
     const bool o_on = ok && n_own > 0;  // (uniform: else O was never written)
     if (o_on) tc_fence_after();
     const uint32_t sw = (uint32_t)(r & 7) << 4;
-    uint8_t* const stg0 = smem + M::stage + r * 512;
-    uint8_t* const stg1 = stg0 + 128 * 512;
+    uint8_t* const stg = smem + M::stage + r * 512;
+    uint8_t* const swap = smem + M::stage + kRowTile * 512 + r * 256;
     auto read_o = [&](int c, float (&o)[32]) {
       if (o_on) {
         uint32_t w[32];
@@ -793,49 +819,46 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
         for (int q = 0; q < 32; ++q) o[q] = ok ? 0.f : NAN;
       }
     };
-    auto stage_o = [&](uint8_t* stg, int c, const float (&o)[32]) {
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        *reinterpret_cast<float4*>(stg + (((8 * c + q) << 4) ^ sw)) =
-            make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-    };
-    float w1 = 0.f;
-    if (t == 1) {
-      if (warp_on) {
+    // each stream joins half of the dimensions, 64 t ..: the other half goes to the other one
+    if (warp_on) {
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          float o[32];
-          read_o(c, o);
-          stage_o(stg1, c, o);
-        }
+      for (int c = 0; c < 2; ++c) {
+        float o[32];
+        read_o(2 * (t ^ 1) + c, o);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          *reinterpret_cast<float4*>(swap + (t ^ 1) * kRowTile * 256 + (((8 * c + q) << 4) ^ sw)) =
+              make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
       }
-      s_row[kRowTile + r] = lse;
     }
+    s_half[tid] = lse;
     sync_rows();
-    if (t == 0) {
-      const float other = s_row[kRowTile + r], mx = fmaxf(lse, other);
+    float w1 = 0.f;
+    {
+      const float other = s_half[tid ^ 128], mx = fmaxf(lse, other);
       const float a0 = lse == -INFINITY ? 0.f : fast_exp2(lse - mx), a1 = other == -INFINITY ? 0.f : fast_exp2(other - mx);
       const float sum = a0 + a1, is = sum == 0.f ? 0.f : 1.f / sum;
       inv *= a0 * is;
       w1 = a1 * is;
       lse = sum == 0.f ? -INFINITY : mx + log2f(sum);
     }
-    if (warp_on && t == 0) {
+    if (warp_on) {
       const bool wild = nt > 0 && (s_vbad[0] | s_vbad[1] | s_vbad[2] | s_vbad[3]);
-      T* out = reinterpret_cast<T*>(a.out) + a.out_row_stride * (first + node) + (size_t)(kvh * G + (qr - node * G)) * kKv8Hd;
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 2 * t; c < 2 * t + 2; ++c) {
         float o[32];
         read_o(c, o);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          const float4 y = *reinterpret_cast<const float4*>(stg1 + (((8 * c + q) << 4) ^ sw));
+          const float4 y = *reinterpret_cast<const float4*>(swap + t * kRowTile * 256 + (((8 * (c & 1) + q) << 4) ^ sw));
           o[4 * q] = fmaf(w1, y.x, o[4 * q]);
           o[4 * q + 1] = fmaf(w1, y.y, o[4 * q + 1]);
           o[4 * q + 2] = fmaf(w1, y.z, o[4 * q + 2]);
           o[4 * q + 3] = fmaf(w1, y.w, o[4 * q + 3]);
         }
         if (wild && row_ok) {  // infinities and NaN in V of the step's own rows, for the rows that see them
+          uint64_t anc0, anc1;
+          seen(anc0, anc1);
 #pragma unroll 1
           for (int k = 0; k <= top; ++k) {
             if (!(s_vbad[k >> 5] >> (k & 31) & 1u)) continue;
@@ -848,22 +871,34 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
             }
           }
         }
-        if (pl.chunks == 1) {
-          if (row_ok) {
-            uint4 w[4];
-            T* e = reinterpret_cast<T*>(w);
+        if (pl.chunks == 1) {  // rounded, so that rows can be written in whole
+          uint4 w[4];
+          T* e = reinterpret_cast<T*>(w);
 #pragma unroll
-            for (int q = 0; q < 32; ++q) e[q] = from_f32<T>(o[q]);
+          for (int q = 0; q < 32; ++q) e[q] = from_f32<T>(o[q]);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) reinterpret_cast<uint4*>(out + 32 * c)[q] = w[q];
-          }
+          for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(smem + M::stage + r * 256 + (((4 * c + q) << 4) ^ sw)) = w[q];
         } else {
-          stage_o(stg0, c, o);
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            *reinterpret_cast<float4*>(stg + (((8 * c + q) << 4) ^ sw)) =
+                make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
         }
       }
-      if (pl.chunks > 1) s_row[r] = lse;
-      else if (row_ok && a.lse)
+      if (t == 0 && pl.chunks > 1) s_row[r] = lse;
+      else if (t == 0 && row_ok && a.lse)
         a.lse[(size_t)(first + node) * a.n_q_heads + kvh * G + (qr - node * G)] = lse * 0.69314718055994531f;
+    }
+    if (pl.chunks == 1) {
+      sync_rows();
+#pragma unroll 4
+      for (int i = 0; i < 8; ++i) {  // half a warp per row
+        const int rr = 16 * warp + 2 * i + (lane >> 4), q2 = row0 + rr, node2 = by_g(q2);
+        const uint4 w = *reinterpret_cast<const uint4*>(smem + M::stage + rr * 256 + (((lane & 15) << 4) ^ ((rr & 7) << 4)));
+        if (q2 < rows)
+          *reinterpret_cast<uint4*>(reinterpret_cast<T*>(a.out) + a.out_row_stride * (first + node2) +
+                                    (size_t)(kvh * G + (q2 - node2 * G)) * kKv8Hd + 8 * (lane & 15)) = w;
+      }
     }
   }
 
@@ -875,15 +910,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
     const int rb = share * per_cta, re = min(valid, rb + per_cta);
     const uint32_t row_base = smem_u32(s_row), stage_base = smem_u32(smem + M::stage);
     static_assert(kKv8TcMaxChunks == 8, "two loads of four parts");
-    for (int rr = rb + warp; rr < re; rr += kThreads / 32) {
+    // half a warp per row, dimensions 4 l .. and 64 + 4 l .. per lane
+    const int l16 = lane & 15;
+    for (int r2 = rb + 2 * warp; r2 < re; r2 += kThreads / 16) {
+      const int rr = min(re - 1, r2 + (lane >> 4));
       const int q2 = row0 + rr, node = by_g(q2);
-      const uint32_t soff = stage_base + (uint32_t)(rr * 512 + ((lane ^ (rr & 7)) << 4));
-      // lane k has part k's log-sum-exp
+      const uint32_t s0 = stage_base + (uint32_t)(rr * 512 + ((l16 ^ (rr & 7)) << 4)), s1 = s0 + 256;
+      // lane k of the half has part k's log-sum-exp
       float x = -INFINITY;
-      if (lane < pl.chunks) x = dsmem_ld_f32(map_peer(row_base + 4 * rr, lane));
-      float4 y[4];
+      if (l16 < pl.chunks) x = dsmem_ld_f32(map_peer(row_base + 4 * rr, l16));
+      float4 y[4][2];
+      auto load = [&](int k0) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) y[k] = dsmem_ld_f4(map_peer(soff, min(k, pl.chunks - 1)));
+        for (int k = 0; k < 4; ++k) {
+          y[k][0] = dsmem_ld_f4(map_peer(s0, min(k0 + k, pl.chunks - 1)));
+          y[k][1] = dsmem_ld_f4(map_peer(s1, min(k0 + k, pl.chunks - 1)));
+        }
+      };
+      load(0);
       float mx = x;
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -892,30 +936,38 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       w *= sum == 0.f ? 0.f : 1.f / sum;
-      if (a.lse && lane == 0)
+      const bool mine = r2 + (lane >> 4) < re;
+      if (a.lse && l16 == 0 && mine)
         a.lse[(size_t)(first + node) * a.n_q_heads + kvh * G + (q2 - node * G)] =
             sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994531f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      float o[8];
 #pragma unroll
-      for (int k0 = 0; k0 < 8; k0 += 4) {
-        if (k0 && pl.chunks <= 4) break;
-        if (k0) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) y[k] = dsmem_ld_f4(map_peer(soff, min(k0 + k, pl.chunks - 1)));
-        }
+      for (int i = 0; i < 8; ++i) o[i] = 0.f;
+#pragma unroll 1
+      for (int k0 = 0; k0 < pl.chunks; k0 += 4) {
+        if (k0) load(k0);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float wk = __shfl_sync(0xffffffffu, w, k0 + k);  // (0 beyond the last part)
-          acc = make_float4(fmaf(wk, y[k].x, acc.x), fmaf(wk, y[k].y, acc.y), fmaf(wk, y[k].z, acc.z), fmaf(wk, y[k].w, acc.w));
+          const float wk = __shfl_sync(0xffffffffu, w, (lane & 16) + k0 + k);  // (0 beyond the last part)
+          const float4 u = y[k][0], v = y[k][1];
+          o[0] = fmaf(wk, u.x, o[0]), o[1] = fmaf(wk, u.y, o[1]), o[2] = fmaf(wk, u.z, o[2]), o[3] = fmaf(wk, u.w, o[3]);
+          o[4] = fmaf(wk, v.x, o[4]), o[5] = fmaf(wk, v.y, o[5]), o[6] = fmaf(wk, v.z, o[6]), o[7] = fmaf(wk, v.w, o[7]);
         }
       }
-      T e[4] = {from_f32<T>(acc.x), from_f32<T>(acc.y), from_f32<T>(acc.z), from_f32<T>(acc.w)};
-      *reinterpret_cast<uint2*>(reinterpret_cast<T*>(a.out) + a.out_row_stride * (first + node) +
-                                (size_t)(kvh * G + (q2 - node * G)) * kKv8Hd + 4 * lane) = *reinterpret_cast<const uint2*>(e);
+      T e[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = from_f32<T>(o[i]);
+      if (mine) {
+        T* const to = reinterpret_cast<T*>(a.out) + a.out_row_stride * (first + node) +
+                      (size_t)(kvh * G + (q2 - node * G)) * kKv8Hd + 4 * l16;
+        *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(e);
+        *reinterpret_cast<uint2*>(to + 64) = *reinterpret_cast<const uint2*>(e + 4);
+      }
     }
   }
   tc_fence_before();
-  if (pl.chunks > 1) cluster_sync_all();  // no CTA leaves while a peer reads it
+  // no CTA leaves while a peer reads it (what was read has been used: nothing to order but the barrier itself)
+  if (pl.chunks > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
   else __syncthreads();
   if (warp == kIssueWarp) {
     tc_fence_after();
