@@ -32,12 +32,13 @@ struct Kv8View {
 cudaError_t kv8_plan_configure();
 cudaError_t launch_kv8_plan(const spec_kv8_plan_args& a, int page_log2, int n_pages, cudaStream_t s);
 cudaError_t launch_kv8_append(const Kv8View& c, const spec_kv8_append_args& a, int sm_count, cudaStream_t s);
-cudaError_t kv8_attention_configure();
+cudaError_t kv8_attention_configure(int sm_count, int* clusters);
 size_t kv8_attention_workspace(const Kv8View& c, int sm_count, int batch, int n_q_heads, int max_nodes, int max_prefix);
-cudaError_t launch_kv8_attention(const Kv8View& c, const CUtensorMap& map, const spec_kv8_attention_args& a, int sm_count, cudaStream_t s);
+cudaError_t launch_kv8_attention(const Kv8View& c, const CUtensorMap& map, const spec_kv8_attention_args& a, const int* clusters, cudaStream_t s);
 
 // rows > 16 per kv head: the tensor-core kernel (prefixes up to kKv8TcMaxChunks * kKv8TcMaxKeys; no workspace)
-cudaError_t kv8_tree_configure();
-cudaError_t launch_kv8_tree(const Kv8View& c, const spec_kv8_attention_args& a, int sm_count, cudaStream_t s);
+// clusters[n]: how many clusters of n CTAs run at once, n = 1 .. kKv8TcMaxChunks
+cudaError_t kv8_tree_configure(int sm_count, int* clusters);
+cudaError_t launch_kv8_tree(const Kv8View& c, const spec_kv8_attention_args& a, const int* clusters, cudaStream_t s);
 
 }  // namespace spec

@@ -19,6 +19,7 @@ struct spec_kv8 {
   uint8_t* exps = nullptr;
   int device = 0;
   int sm_count = 148;
+  int clusters[kKv8TcMaxChunks + 1] = {};  // of the tree kernel: see kv8_tree_configure
   int page_log2 = 4;
   CUtensorMap map;  // the codes as rows of 128 bytes, boxes of 16 rows, 128-byte swizzle
   char err[256] = "";
@@ -124,12 +125,12 @@ int spec_kv8_open(const spec_kv8_config* cfg, void* codes, size_t code_bytes, vo
   if (!config_ok(cfg) || !codes || !exps || (reinterpret_cast<uintptr_t>(codes) & 127u)) return SPEC_ERR_ARG;
   if (code_bytes < spec_kv8_code_bytes(cfg) || exp_bytes < spec_kv8_exp_bytes(cfg)) return SPEC_ERR_CAPACITY;
   // without a GPU the handle still checks its calls' arguments; they end in SPEC_ERR_CUDA
-  int dev = -1, sms = 148;
+  int dev = -1, sms = 148, clusters[kKv8TcMaxChunks + 1] = {};
   if (cudaGetDevice(&dev) != cudaSuccess) {
     dev = -1;
     (void)cudaGetLastError();
   } else if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-             kv8_plan_configure() != cudaSuccess || kv8_attention_configure() != cudaSuccess) {
+             kv8_plan_configure() != cudaSuccess || kv8_attention_configure(sms, clusters) != cudaSuccess) {
     return SPEC_ERR_CUDA;
   }
   spec_kv8* h = new (std::nothrow) spec_kv8;
@@ -143,6 +144,8 @@ int spec_kv8_open(const spec_kv8_config* cfg, void* codes, size_t code_bytes, vo
   h->exps = static_cast<uint8_t*>(exps);
   h->device = dev;
   h->sm_count = sms;
+  for (int n = 0; n <= kKv8TcMaxChunks; ++n) h->clusters[n] = clusters[n];
+  h->clusters[1] = sms;
   while ((1 << h->page_log2) < cfg->page) ++h->page_log2;
   *out = h;
   return SPEC_OK;
@@ -235,7 +238,7 @@ int spec_kv8_attention(spec_kv8* h, int layer, const spec_kv8_attention_args* a,
   if (int rc = check_device(h)) return rc;
   spec_kv8_attention_args b = *a;
   if (b.scale == 0.f) b.scale = 0.08838834764831845f;  // 1 / sqrt(128)
-  return launched(h, launch_kv8_attention(view_of(h, layer), h->map, b, h->sm_count, static_cast<cudaStream_t>(cuda_stream)),
+  return launched(h, launch_kv8_attention(view_of(h, layer), h->map, b, h->clusters, static_cast<cudaStream_t>(cuda_stream)),
                   "attention");
 }
 

@@ -554,20 +554,20 @@ size_t kv8_attention_workspace(const Kv8View& c, int sm_count, int batch, int n_
   return bytes;
 }
 
-cudaError_t kv8_attention_configure() {
-  cudaError_t e = kv8_tree_configure();
+cudaError_t kv8_attention_configure(int sm_count, int* clusters) {
+  cudaError_t e = kv8_tree_configure(sm_count, clusters);
   for (const void* f : {(const void*)kv8_decode_kernel<__nv_bfloat16, 1>, (const void*)kv8_decode_kernel<__nv_bfloat16, 2>,
                         (const void*)kv8_decode_kernel<__half, 1>, (const void*)kv8_decode_kernel<__half, 2>})
     if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::dyn);
   return e;
 }
 
-cudaError_t launch_kv8_attention(const Kv8View& c, const CUtensorMap& map, const spec_kv8_attention_args& a, int sm_count,
+cudaError_t launch_kv8_attention(const Kv8View& c, const CUtensorMap& map, const spec_kv8_attention_args& a, const int* clusters,
                                  cudaStream_t s) {
-  if (by_tree(c.hkv, a.n_q_heads, a.max_nodes, a.max_prefix)) return launch_kv8_tree(c, a, sm_count, s);
+  if (by_tree(c.hkv, a.n_q_heads, a.max_nodes, a.max_prefix)) return launch_kv8_tree(c, a, clusters, s);
   int nt = 1;
   size_t bytes = 0;
-  DecodePlan p = plan_decode(c.hkv, sm_count, a.batch, a.n_q_heads, a.max_nodes, a.max_prefix, &nt, &bytes);
+  DecodePlan p = plan_decode(c.hkv, clusters[1], a.batch, a.n_q_heads, a.max_nodes, a.max_prefix, &nt, &bytes);
   const int per_launch = p.group0;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   p.counters = reinterpret_cast<int*>(ws);

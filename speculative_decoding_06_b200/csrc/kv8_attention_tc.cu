@@ -7,7 +7,9 @@
 // the units in turn, each with its own running maximum, sum and output; they join
 // at the end.
 //
-//   loader (1 thread)     bulk copies of the codes of a unit, three units deep.
+//   loader (1 thread)     bulk copies of the codes of a unit, three units deep, the first ones as soon as its warp
+//       has looked up their pages.
+//   helper (1 warp)       the tree's ancestor sets.
 //   converters (4 warps for K, 4 for V)  turn codes into fp16 (exact) and write them as
 //       the swizzled K and V operands.  K and V of the step's own rows become fp16
 //       times a power of two that their largest value sets.
@@ -19,15 +21,16 @@
 // What bounds it: a unit takes 0.59 us of a CTA, 1050 cycles, of which the MMAs need
 // 512, the exponentials 512 of the special-function units, shared memory 770 (codes in and out, operands in and out)
 // and the instructions of softmax and conversion some 700 of the issue slots; the rest is the latency of a unit's
-// chain (codes to operand, tensor memory to registers and back, six barriers).  Start and end of a CTA take 13 us.
-// 4 prompts of 6150 - 8192 tokens, 128 rows x 8 kv heads x 4: 89 us, 700 TFLOP/s.
+// chain (codes to operand, tensor memory to registers and back, six barriers).  Start and end of a CTA take 9 us, with
+// a cluster's join 10 - 13.  4 prompts of 6150 - 8192 tokens, 128 rows x 8 kv heads x 4: 91 us, 680 TFLOP/s.
 // Tried and slower: one issuer for both streams, which keeps them in step, so that both want the special-function
 // units at once (0.95 us a unit); codes by cp.async of the converters (0.95 us); four threads per row, whose
 // exchange of maxima costs what it saves (0.97 us); 128-key score tiles (0.97 us); q in shared memory, read again
 // for every unit (0.03 us more).  Two row tiles that share a unit's conversion took 11 % less per row than one did
 // then, but need twice the rows.  Tiles cut by their work, so that each SM has as many units, with parts joined by
 // the last CTA to arrive: a second tile per CTA and the joining cost 19 us, more than the even load gave (the four
-// prompts 104 us, 16 trees 89 us).
+// prompts 104 us, 16 trees 89 us, when they took 94 and 79).  q by one bulk copy per row (128 copies of 256 bytes take
+// 5 us), or read in half rows, a thread each (2000 cycles of the load pipe).
 //
 // Scales: the unit's K exponent (the largest of its pages'; codes of a page with a
 // smaller one are multiplied by the difference as they are converted, exact to
@@ -976,55 +979,77 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
 }
 
 template <typename T>
-cudaError_t launch_tree(const Kv8View& c, const spec_kv8_attention_args& a, const TcPlan& p, int row_tiles,
-                        cudaStream_t s) {
+cudaLaunchConfig_t tree_config(dim3 grid, int chunks, cudaLaunchAttribute* attr) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.chunks * row_tiles, c.hkv, a.batch);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = M::dyn;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = p.chunks;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = chunks;
+  attr->val.clusterDim.y = 1;
+  attr->val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = p.chunks > 1 ? 1 : 0;
+  cfg.numAttrs = chunks > 1 ? 1 : 0;
+  return cfg;
+}
+
+template <typename T>
+cudaError_t launch_tree(const Kv8View& c, const spec_kv8_attention_args& a, const TcPlan& p, int row_tiles,
+                        cudaStream_t s) {
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = tree_config<T>(dim3(p.chunks * row_tiles, c.hkv, a.batch), p.chunks, attr);
+  cfg.stream = s;
   return cudaLaunchKernelEx(&cfg, kv8_tree_kernel<T>, c, a, p);
 }
 
 template <typename T>
-cudaError_t configure_tree() {
+cudaError_t configure_tree(int sm_count, int* clusters) {
   cudaError_t e = cudaFuncSetAttribute(kv8_tree_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)M::dyn);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(kv8_tree_kernel<T>, cudaFuncAttributePreferredSharedMemoryCarveout,
                              (int)cudaSharedmemCarveoutMaxShared);
+  // how many clusters of n CTAs the GPU holds at once
+  clusters[0] = 0, clusters[1] = sm_count;
+  for (int n = 2; n <= kKv8TcMaxChunks && e == cudaSuccess; ++n) {
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = tree_config<T>(dim3(n), n, attr);
+    e = cudaOccupancyMaxActiveClusters(&clusters[n], kv8_tree_kernel<T>, &cfg);
+  }
   return e;
 }
 
 }  // namespace
 
-cudaError_t kv8_tree_configure() {
-  cudaError_t e = configure_tree<__nv_bfloat16>();
-  return e == cudaSuccess ? configure_tree<__half>() : e;
+cudaError_t kv8_tree_configure(int sm_count, int* clusters) {
+  const cudaError_t e = configure_tree<__nv_bfloat16>(sm_count, clusters);
+  return e == cudaSuccess ? configure_tree<__half>(sm_count, clusters) : e;
 }
 
-cudaError_t launch_kv8_tree(const Kv8View& c, const spec_kv8_attention_args& a, int sm_count, cudaStream_t s) {
+cudaError_t launch_kv8_tree(const Kv8View& c, const spec_kv8_attention_args& a, const int* clusters, cudaStream_t s) {
   const int G = a.n_q_heads / c.hkv;
   const int row_tiles = (a.max_nodes * G + kRowTile - 1) / kRowTile;
   const long long tiles = (long long)a.batch * c.hkv * row_tiles;
   const int units = (a.max_prefix + kKeys - 1) / kKeys;
-  // A cluster shares a prefix only while SMs would idle, and a share is at least eight units: joining shares takes
-  // 4 us, as long as five units (one tree of 61 nodes, 2048 tokens, 16 tiles: 32 us with one CTA each, 26, 20 and 21
-  // with 2, 4 and 6; 192 tiles of 512 - 4096 tokens: 83 us with one, 95 with two).  More tiles than SMs start with the
-  // longest (16 trees, 192 tiles of 630 - 4096 tokens: 78 us, 82 in the batch's order)
-  long long chunks = tiles > sm_count ? 1 : sm_count / tiles;
-  chunks = chunks < units / 8 ? chunks : units / 8;
-  chunks = chunks < 1 ? 1 : chunks > kKv8TcMaxChunks ? kKv8TcMaxChunks : chunks;
+  // The CTAs of a cluster share a prefix where that is sooner done: rounds of clusters that the GPU holds at once, each
+  // as long as a share's units and a cluster's start, join and end, all in units of 0.6 us.  Measured with bf16 trees, us:
+  //   CTAs of a cluster (clusters at once)   1 (148)  2 (74)  3 (45)  4 (33)  5 (26)  6 (22)  7 (15)  8 (15)
+  //    8 tiles, 2048 tokens                    28.8    20.9    17.6    15.3    17.1    15.8    14.3    13.6
+  //   16 tiles, 1024 tokens                    19.3    17.4    15.7    13.3    17.4    16.1    27.1    25.2
+  //   16 tiles, 8192 tokens                    86.5    51.2    38.1    30.7    31.2    28.5    47.0    43.1
+  //   64 tiles, 4096 tokens                    49.0    33.4    50.6    43.7    70.2    63.2    90.3    82.7
+  static constexpr int kEnds[kKv8TcMaxChunks + 1] = {0, 15, 19, 18, 17, 22, 21, 18, 17};
   const int need = (a.max_prefix + kKv8TcMaxKeys - 1) / kKv8TcMaxKeys;
   TcPlan p;
-  p.by_length = a.batch > 1 && a.batch <= kByLength && tiles > sm_count;
-  p.chunks = chunks < need ? need : (int)chunks;
+  p.chunks = need < 1 ? 1 : need;
+  long long best = -1;
+  for (int n = p.chunks; n <= kKv8TcMaxChunks; ++n) {
+    if (clusters[n] < 1) continue;
+    const long long cost = (tiles + clusters[n] - 1) / clusters[n] * (kEnds[n] + (units + 2 + n - 1) / n);
+    if (best < 0 || cost < best) best = cost, p.chunks = n;
+  }
+  // more tiles than SMs start with the longest prefixes (16 trees, 192 tiles of 630 - 4096 tokens: 78 us, 82 in the
+  // batch's order)
+  p.by_length = a.batch > 1 && a.batch <= kByLength && tiles > clusters[1];
   p.by_chunks = (uint32_t)((((uint64_t)1 << 32) + p.chunks - 1) / p.chunks);
   p.by_group = (uint32_t)(((1u << 20) + G - 1) / G);
   return a.dtype == SPEC_DTYPE_BF16 ? launch_tree<__nv_bfloat16>(c, a, p, row_tiles, s)
