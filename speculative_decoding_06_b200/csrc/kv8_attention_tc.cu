@@ -1037,12 +1037,14 @@ cudaError_t launch_kv8_tree(const Kv8View& c, const spec_kv8_attention_args& a, 
   //   16 tiles, 1024 tokens                    19.3    17.4    15.7    13.3    17.4    16.1    27.1    25.2
   //   16 tiles, 8192 tokens                    86.5    51.2    38.1    30.7    31.2    28.5    47.0    43.1
   //   64 tiles, 4096 tokens                    49.0    33.4    50.6    43.7    70.2    63.2    90.3    82.7
+  // More tiles than SMs have a CTA each: ragged batches have fewer and shorter ones than the bounds say (10 trees of
+  // 16 - 61 over 512 - 4096 tokens, 160 tiles by their bounds: 51 us with one, 60 with two; equal ones 101 with either).
   static constexpr int kEnds[kKv8TcMaxChunks + 1] = {0, 15, 19, 18, 17, 22, 21, 18, 17};
-  const int need = (a.max_prefix + kKv8TcMaxKeys - 1) / kKv8TcMaxKeys;
+  const int least = a.max_prefix > kKv8TcMaxKeys ? (a.max_prefix + kKv8TcMaxKeys - 1) / kKv8TcMaxKeys : 1;
   TcPlan p;
-  p.chunks = need < 1 ? 1 : need;
+  p.chunks = least;
   long long best = -1;
-  for (int n = p.chunks; n <= kKv8TcMaxChunks; ++n) {
+  for (int n = least; n <= (tiles > clusters[1] ? least : kKv8TcMaxChunks); ++n) {
     if (clusters[n] < 1) continue;
     const long long cost = (tiles + clusters[n] - 1) / clusters[n] * (kEnds[n] + (units + 2 + n - 1) / n);
     if (best < 0 || cost < best) best = cost, p.chunks = n;
