@@ -520,12 +520,13 @@ DecodePlan plan_decode(int hkv, int sm_count, int batch, int n_q_heads, int max_
   *nt = rows <= 8 ? 1 : 2;
   p.row_tiles = (rows + 8 * *nt - 1) / (8 * *nt);
   const long long groups = (long long)batch * hkv * p.row_tiles;
-  // One round of three CTAs per SM where that makes chunks of up to 1024 keys: a CTA's start, end and partial result
-  // take some 5 us.  With more work than that, shares of an eighth of an SM's keys, for an even load (prefixes of one
-  // length assumed: ragged ones make fewer CTAs).  64 sequences x 8 heads of 512 - 4096 tokens: 60.5 us with eighths,
-  // 66.6 with quarters, 63.6 with sixteenths.  At least a tile for each warp.
+  // One round of three CTAs per SM where that makes chunks of up to 2048 keys: a CTA's start, end and partial result
+  // take some 5 us (1 x 65536 tokens x 8 heads: 33 us, 43 with chunks of 1024, which are two rounds; 7 x 16385 x 4: 29
+  // and 36; the same ragged, 1 - 16385: 24 and 23).  With more work than that, shares of an eighth of an SM's keys, for
+  // an even load (prefixes of one length assumed: ragged ones make fewer CTAs).  64 sequences x 8 heads of 512 - 4096
+  // tokens: 60.5 us with eighths, 66.6 with quarters, 63.6 with sixteenths.  At least a tile for each warp.
   long long want = groups * max_prefix / (3LL * sm_count);
-  if (want > 1024) want = groups * max_prefix / (8LL * sm_count) > 1024 ? groups * max_prefix / (8LL * sm_count) : 1024;
+  if (want > 2048) want = groups * max_prefix / (8LL * sm_count) > 1024 ? groups * max_prefix / (8LL * sm_count) : 1024;
   long long chunk = (want + 127) / 128 * 128;
   chunk = chunk < 128 ? 128 : chunk > kMaxChunk ? kMaxChunk : chunk;
   p.chunk = (int)chunk;

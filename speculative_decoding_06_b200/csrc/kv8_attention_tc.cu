@@ -623,10 +623,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
     const int r = (warp & 3) * 32 + lane;    // TMEM lane
     const bool warp_on = __any_sync(0xffffffffu, row0 + r < rows);
     // what the row sees of the step's own rows, in the last of the rounds' buffers
+    bool ok = true;
     auto seen = [&](uint64_t& lo, uint64_t& hi) {
       const int node = row0 + r < rows ? by_g(row0 + r) : 0;
       if (a.parents) {
-        held(B_ANC, 0);
+        if (!held(B_ANC, 0)) ok = false;
         const ulonglong2 set = s_anc[128 * ((32 - __clz(top)) & 1) + node];
         lo = set.x, hi = set.y;
       } else {
@@ -638,7 +639,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
     // largest finite value of both halves sets
     float* const s_half = reinterpret_cast<float*>(smem + M::half);
     float qs = a.scale * 1.4426950408889634f;
-    bool ok = true;
     {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
