@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
         }
       }
       if (ok) {
-        tc_commit(&bar[B_O]);
+        if (nu > 0) tc_commit(&bar[B_O]);  // (without units nobody waits for it: it could land in released memory)
       } else {
         *abort_flag = 1;
         tc_commit(&bar[B_DRAIN + t]);  // issued MMAs finish before the CTA's memory is released

@@ -428,6 +428,21 @@ def test_attention_with_idle_warps_repeats(nodes, prefix, dtype):
     assert int(wrong) == 0
 
 
+@pytest.mark.parametrize("prefixes,nodes,bound", [([0, 0, 70], [20, 17, 30], 70), ([0], [40], 20000),
+                                                  ([65, 0, 1], [33, 18, 17], 6000)])
+def test_attention_of_tiles_without_units(prefixes, nodes, bound):
+    """No prefix and no rows of its own, alone and beside tiles that have some; shares of a cluster's bound of which only
+    the first holds keys.  Again and again, so that a CTA follows another one in the same shared memory."""
+    c = attention_case(25, prefixes, nodes, 8, 2, 64, "bf16", "none")
+    blocks = -(-bound // 64)
+    c["tables"] = np.pad(c["tables"], ((0, 0), (0, max(0, blocks - c["tables"].shape[1]))), constant_values=-1)
+    first, ref = run_attention(c, max_prefix=bound), reference(c)
+    check_attention(c, first, ref)
+    for _ in range(50):
+        again = run_attention(c, max_prefix=bound)
+    assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
+
+
 def test_refusals_of_the_torch_side():
     c = attention_case(17, [40], [2], 4, 2, 16, "bf16")
     cache, q = c["cache"], c["q"].cuda()
