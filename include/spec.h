@@ -524,9 +524,9 @@ typedef struct spec_kv8_attention_args {
   const int32_t* seq_ids;  /* [batch], or NULL: entry b is sequence b */
   void* out;               /* [rows][n_q_heads][128], contiguous but for out_row_stride */
   float* lse;              /* [rows][n_q_heads], or NULL */
-  void* workspace;         /* spec_kv8_attention_workspace() bytes, zero before its first use, then for calls of
-                              any bounds that it is large enough for; calls (or graphs) that may overlap on the
-                              GPU need one each */
+  void* workspace;         /* spec_kv8_attention_workspace() bytes, the first SPEC_KV8_WORKSPACE_ZERO of them zero
+                              before its first use (not between calls, whatever their bounds); calls (or graphs)
+                              that may overlap on the GPU need one each */
   size_t workspace_bytes;
   int64_t q_row_stride, q_head_stride, k_row_stride, k_head_stride, v_row_stride, v_head_stride,
       out_row_stride;      /* in elements; rows of 16-byte alignment */
@@ -540,7 +540,9 @@ typedef struct spec_kv8_attention_args {
   int32_t max_prefix;      /* no lengths[s] is above this (entries above it are left as they were) */
   float scale;             /* > 0; 0: 1 / sqrt(128) */
 } spec_kv8_attention_args;
-/* Workspace bytes of spec_kv8_attention for these bounds. */
+#define SPEC_KV8_WORKSPACE_ZERO 65536
+/* Workspace bytes of spec_kv8_attention for these bounds and for all calls whose bounds are none of them above these:
+ * a program makes one workspace for its largest batch, trees and prefixes (0: bounds rejected). */
 SPEC_API size_t spec_kv8_attention_workspace(spec_kv8* h, int batch, int n_q_heads, int max_nodes, int max_prefix);
 SPEC_API int spec_kv8_attention(spec_kv8* h, int layer, const spec_kv8_attention_args* a, void* cuda_stream);
 

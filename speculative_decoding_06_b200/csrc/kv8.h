@@ -33,6 +33,8 @@ cudaError_t kv8_plan_configure();
 cudaError_t launch_kv8_plan(const spec_kv8_plan_args& a, int page_log2, int n_pages, cudaStream_t s);
 cudaError_t launch_kv8_append(const Kv8View& c, const spec_kv8_append_args& a, int sm_count, cudaStream_t s);
 cudaError_t kv8_attention_configure(int sm_count, int* clusters);
+// workspace bytes that a call of these bounds needs; that every call up to these bounds needs
+size_t kv8_attention_need(const Kv8View& c, int sm_count, int batch, int n_q_heads, int max_nodes, int max_prefix);
 size_t kv8_attention_workspace(const Kv8View& c, int sm_count, int batch, int n_q_heads, int max_nodes, int max_prefix);
 cudaError_t launch_kv8_attention(const Kv8View& c, const CUtensorMap& map, const spec_kv8_attention_args& a, const int* clusters, cudaStream_t s);
 

@@ -233,7 +233,8 @@ int spec_kv8_attention(spec_kv8* h, int layer, const spec_kv8_attention_args* a,
     return fail(h, SPEC_ERR_ARG, "q, k_new, v_new and out rows must be 16-byte aligned, with strides of whole 16-byte units");
   if (a->out_row_stride < (int64_t)a->n_q_heads * kKv8Hd) return fail(h, SPEC_ERR_ARG, "out rows overlap");
   if (!a->workspace || !aligned16(a->workspace)) return fail(h, SPEC_ERR_ARG, "workspace is null or not 16-byte aligned");
-  if (a->workspace_bytes < spec_kv8_attention_workspace(h, a->batch, a->n_q_heads, a->max_nodes, a->max_prefix))
+  if (a->workspace_bytes <
+      kv8_attention_need(view_of(h, 0), h->sm_count, a->batch, a->n_q_heads, a->max_nodes, a->max_prefix))
     return fail(h, SPEC_ERR_CAPACITY, "workspace too small");
   if (int rc = check_device(h)) return rc;
   spec_kv8_attention_args b = *a;

@@ -53,6 +53,7 @@ constexpr int kGroups = kMaxChunk / 16;
 // Workspace: arrival counters at its start, wherever a call's bounds put the rest, so that they are zero between calls
 // of any bounds; then (m, l) and O of every (group, chunk).
 constexpr int kMaxGroups = 16384;  // groups (sequence, kv head, row tile) of one launch
+static_assert(4 * kMaxGroups == SPEC_KV8_WORKSPACE_ZERO, "counters");
 struct DecodePlan {
   int chunk, chunks, row_tiles;
   int group0, groups;  // of this launch, of all
@@ -547,12 +548,33 @@ bool by_tree(int hkv, int n_q_heads, int max_nodes, int max_prefix) {
 
 }  // namespace
 
-size_t kv8_attention_workspace(const Kv8View& c, int sm_count, int batch, int n_q_heads, int max_nodes, int max_prefix) {
+size_t kv8_attention_need(const Kv8View& c, int sm_count, int batch, int n_q_heads, int max_nodes, int max_prefix) {
   if (by_tree(c.hkv, n_q_heads, max_nodes, max_prefix)) return 16;
   int nt = 1;
   size_t bytes = 0;
   plan_decode(c.hkv, sm_count, batch, n_q_heads, max_nodes, max_prefix, &nt, &bytes);
   return bytes;
+}
+
+// At least what every call needs whose bounds are none of them above these.  With g groups and prefixes of p keys a call
+// keeps g * chunks partial results of 8 or 16 rows where it has more than one chunk:
+//   chunks of kMaxChunk keys (p above it): g * ceil(p / kMaxChunk), which grows with both;
+//   shorter ones: chunks < p / chunk + 1, and chunk is above 1024 / 1025 of g p / (8 SMs) (of g p / (3 SMs), 128 / 129),
+//   so that g p / chunk < 9 SMs; more than one chunk means p > chunk and so g < 9 SMs: less than min(g, 9 SMs) + 9 SMs.
+// More than 16 rows come here only with prefixes that the tree kernel does not take; below them its calls need nothing,
+// but those of fewer rows do.
+size_t kv8_attention_workspace(const Kv8View& c, int sm_count, int batch, int n_q_heads, int max_nodes, int max_prefix) {
+  const int rows = max_nodes * (n_q_heads / c.hkv);
+  const int nt = rows <= 8 ? 1 : 2;
+  const int tiles = rows <= 16 || by_tree(c.hkv, n_q_heads, max_nodes, max_prefix) ? 1 : (rows + 15) / 16;
+  const long long groups = (long long)batch * c.hkv * tiles, held = groups < kMaxGroups ? groups : kMaxGroups;
+  const long long round = 9LL * sm_count;
+  long long slots = (groups < round ? groups : round) + round;
+  if (max_prefix > kMaxChunk) {
+    const long long longest = held * (((long long)max_prefix + kMaxChunk - 1) / kMaxChunk);
+    if (longest > slots) slots = longest;
+  }
+  return 4 * kMaxGroups + (size_t)slots * 8 * nt * (kKv8Hd * 4 + 8);
 }
 
 cudaError_t kv8_attention_configure(int sm_count, int* clusters) {

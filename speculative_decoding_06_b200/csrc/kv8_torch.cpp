@@ -9,6 +9,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 #include <exception>
@@ -245,7 +246,8 @@ PyObject* py_attention(PyObject*, PyObject* const* p, Py_ssize_t n) {
     a.lse = lse->data_ptr<float>();
     if (!ws) {
       const size_t bytes = spec_kv8_attention_workspace(c.h, a.batch, a.n_q_heads, a.max_nodes, a.max_prefix);
-      new_ws = at::zeros({(int64_t)bytes}, q.options().dtype(at::kByte));
+      new_ws = at::empty({(int64_t)bytes}, q.options().dtype(at::kByte));
+      if (bytes) new_ws.narrow(0, 0, std::min<int64_t>(bytes, SPEC_KV8_WORKSPACE_ZERO)).zero_();
       ws = &new_ws;
     }
     on_device(*ws, c, "workspace");

@@ -135,8 +135,9 @@ class KV8Cache:
             self._fail(rc)
 
     def attention_workspace(self, batch: int, n_q_heads: int, max_nodes: int, max_prefix: int) -> torch.Tensor:
-        """A workspace for attention() within these bounds.  A program keeps one per stream; calls (or graphs) that
-        may run at the same time need one each."""
+        """A workspace for attention() within these bounds: for fewer sequences or nodes and shorter prefixes too.  A
+        program keeps one per stream, made for its largest bounds; calls (or graphs) that may run at the same time need
+        one each."""
         n = S.spec_kv8_attention_workspace(self.h, batch, n_q_heads, max_nodes, max_prefix)
         if n == 0:
             raise S.SpecError(S.SPEC_ERR_ARG, "attention bounds rejected")

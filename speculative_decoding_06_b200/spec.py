@@ -39,6 +39,8 @@ SPEC_KV8_ROWS = 1
 SPEC_KV8_PAGES = 2
 SPEC_KV8_TABLE = 4
 SPEC_KV8_INDEX = 8
+# bytes at the start of an attention workspace that have to be zero before its first use
+SPEC_KV8_WORKSPACE_ZERO = 65536
 
 PROF_CLASSES = ("embed_meta", "gemm_qkv", "rope_kv_store", "attention", "gemm_o", "resid_norm", "gemm_gate_up",
                 "gemm_down", "lm_head", "lm_reduce", "accept_walk", "kv_compact", "gemm_layer", "draft_fc", "topk",

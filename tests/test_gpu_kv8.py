@@ -537,3 +537,18 @@ def test_pages_beyond_32_bit_offsets(nodes):
     out = cache.attention(0, c["q"].cuda(), i32([used]), i32([P]), i32([0, nodes]), max_prefix=P, max_nodes=nodes)
     check_attention(c, out, O.attention(codes, exps, page, c["q"].double().numpy(), np.array([[0, 1]]), [P], [0, nodes],
                                         128 ** -0.5))
+
+
+def test_workspace_of_the_largest_bounds_serves_a_draining_batch():
+    """A batch that shrinks, trees between plain steps: one workspace, made for the most of each bound and full of
+    something else behind its zeros, for all of them."""
+    ws = None
+    for B, n, top in ((40, 20, 900), (40, 1, 900), (39, 1, 700), (7, 3, 900), (1, 1, 900), (1, 20, 64), (12, 2, 300)):
+        g = np.random.default_rng(B)
+        prefixes = [int(x) for x in g.integers(1, top + 1, B)]
+        prefixes[-1] = top
+        c = attention_case(26, prefixes, [n] * B, 8, 2, 32, "bf16")
+        if ws is None:
+            ws = c["cache"].attention_workspace(40, 8, 20, 900)
+            ws[S.SPEC_KV8_WORKSPACE_ZERO:] = 0x7F
+        check_attention(c, run_attention(c, workspace=ws), reference(c))

@@ -197,3 +197,46 @@ def test_attention_refusals(handle, layer, kw, rc):
     a = S.spec_kv8_attention_args(**{**ATTN, **kw})
     assert S.spec_kv8_attention(handle, layer, ctypes.byref(a), None) == rc
     assert S.spec_kv8_attention(handle, layer, None, None) == S.SPEC_ERR_ARG
+
+
+# ---------------------------------------------------------------- workspaces
+def workspace(h, batch, n_q_heads, max_nodes, max_prefix):
+    return S.spec_kv8_attention_workspace(h, batch, n_q_heads, max_nodes, max_prefix)
+
+
+def test_workspace_grows_with_every_bound(handle):
+    """A workspace made for a program's largest bounds is large enough for every call below them: fewer sequences, fewer
+    nodes (the other kernel too), shorter prefixes (one chunk or many)."""
+    g = np.random.default_rng(1)
+    batches = sorted({1, 2, 46, 47, 64, 128, 255, 256, 512, 4096, 65535, *np.exp(g.uniform(0, 11, 20)).astype(int).tolist()})
+    prefixes = sorted({0, 1, 128, 129, 1024, 2048, 2049, 4096, 4097, 131072, 393216, 393217,
+                       *np.exp(g.uniform(0, 14, 40)).astype(int).tolist()})
+    nodes = [1, 2, 3, 4, 5, 8, 9, 61, 128]
+    size = np.array([[[workspace(handle, b, 8, n, p) for p in prefixes] for n in nodes] for b in batches], dtype=np.float64)
+    assert size.min() >= 16
+    for axis in range(3):
+        assert (np.diff(size, axis=axis) >= 0).all()
+
+
+@pytest.mark.parametrize("large,small", [
+    ((47, 1, 4096), (46, 1, 4096)), ((64, 61, 4096), (64, 1, 4096)), ((256, 1, 2048), (128, 1, 2048)),
+    ((512, 1, 1024), (8, 1, 1024)), ((1, 128, 200000), (1, 4, 131072)), ((2000, 1, 9000), (300, 2, 4100)),
+    ((9000, 128, 393217), (9000, 8, 393216)), ((64, 16, 4096), (64, 15, 4000))])
+def test_workspace_of_larger_bounds_serves_smaller_calls(handle, large, small):
+    args = {**ATTN, "seq_ids": 4096, "max_blocks": 8192}
+    for batch, nodes, prefix in (large, small):
+        a = S.spec_kv8_attention_args(**{**args, "batch": batch, "max_nodes": nodes, "max_prefix": prefix,
+                                         "workspace_bytes": workspace(handle, large[0], 8, large[1], large[2])})
+        assert S.spec_kv8_attention(handle, 0, ctypes.byref(a), None) == S.SPEC_ERR_CUDA, S.spec_kv8_last_error(handle)
+
+
+def test_workspace_of_random_bounds_serves_all_below_them(handle):
+    g = np.random.default_rng(2)
+    for _ in range(3000):
+        large = [int(np.exp(g.uniform(0, np.log(top + 1)))) for top in (65535, 128, 500000)]
+        small = [max(1, int(x * g.choice([1.0, 0.999, g.random(), np.exp(-8 * g.random())]))) for x in large]
+        for hq in (4, 16, 64):
+            a = S.spec_kv8_attention_args(**{**ATTN, "seq_ids": 4096, "max_blocks": 8192, "batch": small[0], "n_q_heads": hq,
+                                             "max_nodes": small[1], "max_prefix": small[2], "out_row_stride": 8192,
+                                             "workspace_bytes": workspace(handle, large[0], 64, large[1], large[2])})
+            assert S.spec_kv8_attention(handle, 0, ctypes.byref(a), None) == S.SPEC_ERR_CUDA, (large, small, hq)
