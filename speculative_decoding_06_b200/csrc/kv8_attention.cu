@@ -13,12 +13,13 @@
 //            k-step's two A registers after e4m3 -> fp16 conversion (exact).
 //   softmax  in 32 bits, base 2.  A page's K scale multiplies the scores; its
 //            V scale 2^w goes into the exponent: p' = 2^(x + w - m), so that O sums
-//            p' times bare codes and l sums p' 2^-w.  m is 7 below the row's running
+//            p' times bare codes and l sums p' 2^(12 - w).  m is 7 below the row's running
 //            maximum of x + w and moves only when exceeded by more than 15: p' <= 2^15,
 //            and fp16, to which p' is rounded (2^-11 of itself) for the second product,
 //            has its full 11 bits down to 2^-21 of the largest p'.  O is divided by the
 //            sum of the rounded p', so that a key's rounding cancels as far as its weight
-//            dominates; the log-sum-exp is that of the unrounded ones.
+//            dominates; the log-sum-exp is that of the unrounded ones.  The weights
+//            do not depend on V, so l has to hold where p' does not: see kLift and kFar.
 //   output   O^T = V^T P^T: lane (g, t) holds dimensions 16g .. 16g+15 of keys 2t,
 //            2t+1, 2t+8, 2t+9; two keys' bytes interleave into A registers;
 //            the scores' accumulators become the B operand by movmatrix.
@@ -49,6 +50,12 @@ constexpr int kStages = 2;
 constexpr int kTileBytes = kTile * 2 * kKv8Hd;
 constexpr int kMaxChunk = 4096;    // keys of a CTA: its page ids and scales lie in shared memory
 constexpr int kGroups = kMaxChunk / 16;
+// l is the sum of 2^(x - m + kLift).  With w in [-60, 120] and m 7 to 22 below the largest x + w, its largest term lies
+// between 2^-101 and 2^87: the sum neither overflows nor loses terms above 2^-25 of the largest.
+constexpr float kLift = 12.f;
+// Keys whose w is that far below the largest so far may have p' = 0 for weights that count in l: l then takes the weights
+// themselves.  (A weight of 2^-43 of the largest has p' of 2^-126 or more at this distance.)
+constexpr float kFar = 90.f;
 
 // Workspace: arrival counters at its start, wherever a call's bounds put the rest, so that they are zero between calls
 // of any bounds; then (m, l) and O of every (group, chunk).
@@ -260,10 +267,11 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_decode_kernel(const __grid_co
   }
   // a row's running maximum rises to m2: what was summed shrinks
   auto raise = [&](int nt, int col, float m2) {
-    const float keep = m2 > m[nt][col] ? fast_exp2(m[nt][col] - m2) : 1.f;
+    const float half = m2 > m[nt][col] ? fast_exp2(0.5f * (m[nt][col] - m2)) : 1.f;
+    const float keep = half * half;
     m[nt][col] = fmaxf(m[nt][col], m2);
-    l[nt][col] *= keep;
-    lr[nt][col] *= keep;
+    l[nt][col] = l[nt][col] * half * half;
+    lr[nt][col] = lr[nt][col] * half * half;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       o[nt][i][col] *= keep;
@@ -272,6 +280,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_decode_kernel(const __grid_co
   };
 
   bool landed = true;
+  float top_w = -INFINITY;  // the largest w so far
   for (int i = 0; i < mine; ++i) {
     landed = __all_sync(0xffffffffu, mbar_wait(&full[i % kStages], (i / kStages) & 1, nullptr, nullptr));
     if (!landed) {  // a wait ran out: copies under way land before the CTA's memory is released, and the rows say so
@@ -300,6 +309,9 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_decode_kernel(const __grid_co
     // x + w in base 2, hidden keys at -inf
     const float ks0 = s_kscale[g0], ks1 = s_kscale[g0 + 1], ve0 = s_vexp[g0], ve1 = s_vexp[g0 + 1];
     const int left = c1 - (c0 + 16 * g0);  // keys of the tile that exist
+    const float low_w = left > 16 ? fminf(ve0, ve1) : ve0;
+    top_w = fmaxf(top_w, left > 16 ? fmaxf(ve0, ve1) : ve0);
+    const bool far = low_w < top_w - kFar;
     uint32_t pb[2][NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -330,16 +342,27 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_decode_kernel(const __grid_co
       const float n0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], n1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const float un = fast_exp2(-(u ? ve1 : ve0));
         const float p0 = fast_exp2(s[u][nt][0] - n0), p1 = fast_exp2(s[u][nt][1] - n1);
         const float p2 = fast_exp2(s[u][nt][2] - n0), p3 = fast_exp2(s[u][nt][3] - n1);
-        l[nt][0] = fmaf(p0 + p2, un, l[nt][0]);
-        l[nt][1] = fmaf(p1 + p3, un, l[nt][1]);
         const __half2 lo = __floats2half2_rn(p0, p1), hi = __floats2half2_rn(p2, p3);
         // (below 2^-14 the rounding loses bits that 2^-w may make matter, and the weight in O is small)
         auto kept = [](float p, float rounded) { return p < 0x1p-14f ? p : rounded; };
-        lr[nt][0] = fmaf(kept(p0, __low2float(lo)) + kept(p2, __low2float(hi)), un, lr[nt][0]);
-        lr[nt][1] = fmaf(kept(p1, __high2float(lo)) + kept(p3, __high2float(hi)), un, lr[nt][1]);
+        if (!far) {
+          const float un = fast_exp2(kLift - (u ? ve1 : ve0));
+          l[nt][0] = fmaf(p0 + p2, un, l[nt][0]);
+          l[nt][1] = fmaf(p1 + p3, un, l[nt][1]);
+          lr[nt][0] = fmaf(kept(p0, __low2float(lo)) + kept(p2, __low2float(hi)), un, lr[nt][0]);
+          lr[nt][1] = fmaf(kept(p1, __high2float(lo)) + kept(p3, __high2float(hi)), un, lr[nt][1]);
+        } else {
+          // (rare) the weights themselves, as squares: 2^-149 where one exponential ends at 2^-126
+          const float w = kLift - (u ? ve1 : ve0);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float h = fast_exp2(0.5f * (s[u][nt][q] - (q & 1 ? n1 : n0) + w));
+            l[nt][q & 1] = fmaf(h, h, l[nt][q & 1]);
+            lr[nt][q & 1] = fmaf(h, h, lr[nt][q & 1]);
+          }
+        }
         pb[u][nt][0] = transpose8x8(*reinterpret_cast<const uint32_t*>(&lo));
         pb[u][nt][1] = transpose8x8(*reinterpret_cast<const uint32_t*>(&hi));
       }
@@ -408,8 +431,13 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_decode_kernel(const __grid_co
           const bool see = __shfl_sync(0xffffffffu, (int)sees, 8 * t + 4 * col);
           if (!see) continue;
           if (xc > m[nt][col] + 15.f) raise(nt, col, xc - 7.f);
-          const float p = fast_exp2(xc - (m[nt][col] == -INFINITY ? 0.f : m[nt][col]));
-          if (g == 0) l[nt][col] += p, lr[nt][col] += p;  // (nothing is rounded here)
+          const float y = xc - (m[nt][col] == -INFINITY ? 0.f : m[nt][col]);
+          const float p = fast_exp2(y);
+          if (g == 0) {  // (nothing is rounded here)
+            const float h = fast_exp2(0.5f * (y + kLift));
+            l[nt][col] = fmaf(h, h, l[nt][col]);
+            lr[nt][col] = fmaf(h, h, lr[nt][col]);
+          }
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             o[nt][i][col] = fmaf(p, v[2 * i], o[nt][i][col]);
@@ -456,13 +484,13 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_decode_kernel(const __grid_co
   // a warp per row, a lane per four dimensions
   auto finish = [&](int r, float mm, float ll, float4 acc) {
     const int node = r / G, head = kvh * G + (r - node * G);
-    const float inv = ll == 0.f ? 0.f : 1.f / ll;
+    const float inv = ll == 0.f ? 0.f : 4096.f / ll;  // 2^kLift
     T* out = reinterpret_cast<T*>(a.out) + a.out_row_stride * (first + node) + (size_t)head * kKv8Hd + 4 * lane;
     T w[4] = {from_f32<T>(acc.x * inv), from_f32<T>(acc.y * inv), from_f32<T>(acc.z * inv), from_f32<T>(acc.w * inv)};
     *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(w);
     if (a.lse && lane == 0)
       a.lse[(size_t)(first + node) * a.n_q_heads + head] =
-          ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f;
+          ll == 0.f ? -INFINITY : (mm - kLift + log2f(ll)) * 0.69314718055994531f;
   };
   const size_t slot = (size_t)group * pl.chunks + chunk_i;
   for (int r = warp; r < kRows && row0 + r < rows; r += kWarps) {
@@ -474,9 +502,9 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_decode_kernel(const __grid_co
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const float2 x = s_ml[w * kRows + r];
-      const float f = x.x == -INFINITY && x.y == 0.f ? 0.f : fast_exp2(x.x - mm);
+      const float h = x.x == -INFINITY && x.y == 0.f ? 0.f : fast_exp2(0.5f * (x.x - mm)), f = h * h;
       const float4 v = *reinterpret_cast<const float4*>(&s_o[(w * kRows + r) * 132 + 4 * lane]);
-      ll = fmaf(f, x.y, ll);
+      ll = fmaf(h, h * x.y, ll);
       acc = make_float4(fmaf(f, v.x, acc.x), fmaf(f, v.y, acc.y), fmaf(f, v.z, acc.z), fmaf(f, v.w, acc.w));
     }
     if (nc == 1) {
@@ -505,8 +533,8 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_decode_kernel(const __grid_co
     for (int k = 0; k < nc; ++k) {
       const float2 x = __ldcg(&pl.ml[(slot0 + k) * kRows + r]);
       const float4 v = __ldcg(reinterpret_cast<const float4*>(pl.part + ((slot0 + k) * kRows + r) * kKv8Hd) + lane);
-      const float f = x.x == -INFINITY && x.y == 0.f ? 0.f : fast_exp2(x.x - mm);
-      ll = fmaf(f, x.y, ll);
+      const float h = x.x == -INFINITY && x.y == 0.f ? 0.f : fast_exp2(0.5f * (x.x - mm)), f = h * h;
+      ll = fmaf(h, h * x.y, ll);
       acc = make_float4(fmaf(f, v.x, acc.x), fmaf(f, v.y, acc.y), fmaf(f, v.z, acc.z), fmaf(f, v.w, acc.w));
     }
     finish(row0 + r, mm, ll, acc);

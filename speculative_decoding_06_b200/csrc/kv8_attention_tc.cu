@@ -38,7 +38,8 @@
 // into the exponential: p' = 2^(x + w - m) with m 7 below a running maximum of x + w,
 // moved only when exceeded by more than 15 (p' <= 2^15, and fp16 has its full 11 bits
 // down to 2^-21 of the largest p'), O sums p' times bare codes and the denominator
-// p' 2^-w.  p' is rounded to fp16 (2^-11 of itself) for the product; O is divided by the
+// p' 2^(12 - w).  The weights do not depend on V, so the denominator has to hold where p' does not: see kLift and kFar.
+// p' is rounded to fp16 (2^-11 of itself) for the product; O is divided by the
 // sum of the rounded p', so that a key's rounding cancels as far as its weight dominates, and
 // the log-sum-exp is that of the unrounded ones.
 //
@@ -70,6 +71,12 @@ constexpr int kStages = 4;    // most operand stages of K or V
 
 constexpr int kByLength = 128;  // most sequences that are put in order
 constexpr int kScores = 3;    // S buffers: unit u has buffer u % 3
+// l is the sum of 2^(x - m + kLift).  With w in [-80, 120] and m 7 to 22 below the largest x + w, its largest term lies
+// between 2^-101 and 2^107: the sum neither overflows nor loses terms above 2^-25 of the largest.
+constexpr float kLift = 12.f;
+// Units whose w is that far below the largest so far may have p' = 0 for weights that count in l: l then takes the weights
+// themselves.  (A weight of 2^-43 of the largest has p' of 2^-126 or more at this distance.)
+constexpr float kFar = 90.f;
 
 // mbarriers: per operand stage; S, P and P V per stream, for its even and its odd units: no wait is for a phase that
 // lies more than one behind what its waiter has seen, however far idle warps of a stream run ahead
@@ -156,9 +163,9 @@ __device__ __forceinline__ uint32_t mul_h2(uint32_t v, __half2 f) {
   return *reinterpret_cast<const uint32_t*>(&y);
 }
 // the exponent that brings values up to `amax` below 2^7 (0 where all are 0)
-__device__ __forceinline__ int shift_of(float amax) {
+__device__ __forceinline__ int shift_of(float amax, int least = -100) {
   const int e = (__float_as_int(amax) >> 23) - 127 - 6;
-  return amax > 0.f ? max(-100, min(120, e)) : 0;
+  return amax > 0.f ? max(least, min(120, e)) : 0;
 }
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
@@ -586,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
 #pragma unroll
       for (int w = 0; w < kConvWarps; ++w) big = max(big, red[w]);
       const uint16_t top_bits = (uint16_t)big;
-      const int shift = shift_of(to_f32<T>(*reinterpret_cast<const T*>(&top_bits)));
+      const int shift = shift_of(to_f32<T>(*reinterpret_cast<const T*>(&top_bits)), p ? -80 : -100);
       if (x == 0) (&s_unit[np + tt].x)[p] = p ? (float)shift : pow2i(shift);
       sync_converters(p);  // (also: everyone has read `red`)
       if (lane == 0) mbar_arrive(&bar[B_TREF + tt]);
@@ -682,6 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
     int sb = t, eo = 2 * t, ph = 0;                                   // the unit's S buffer, barrier and phase
     const int n_own = (nu - t + 1) >> 1;  // the stream's units
     float m = -INFINITY, l = 0.f, lr = 0.f;  // lr: of the rounded probabilities
+    float top_w = -INFINITY;                 // the largest w so far
 #pragma unroll 1
     for (int i = 0; i < n_own; ++i) {
       const int u = 2 * i + t;
@@ -700,7 +708,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
       }
       const float2 e = s_unit[u];
       const float f = qs * e.x, ve = e.y;
-      const float un = fast_exp2(-ve);
+      const bool far = ve < top_w - kFar;  // (of all threads alike)
+      top_w = fmaxf(top_w, ve);
       if (ok) ok = held(B_SFULL + eo, ph);
       ok = __all_sync(0xffffffffu, ok);
       if (ok && warp_on) {
@@ -735,10 +744,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
         const bool up = mx > m + 15.f;
         if (__any_sync(0xffffffffu, up)) {
           mx -= 7.f;
-          const float keep = up ? fast_exp2(m - mx) : 1.f;
+          const float half = up ? fast_exp2(0.5f * (m - mx)) : 1.f, keep = half * half;
           m = up ? mx : m;
-          l *= keep;
-          lr *= keep;
+          l = l * half * half;
+          lr = lr * half * half;
           if (i > 0) {
             // O shrinks: the product of the stream's last unit has to be in it
             ok = __all_sync(0xffffffffu, held(B_PV + 2 * t + ((i - 1) & 1), ((i - 1) >> 1) & 1));
@@ -756,33 +765,62 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
             }
           }
         }
-        const float add = ve - (m == -INFINITY ? 0.f : m);
-        const uint64_t f2 = f2_pack(f, f), a2 = f2_pack(add, add);
-        uint64_t l0 = f2_pack(0.f, 0.f);
-        float r0 = 0.f, r1 = 0.f;  // of the rounded probabilities
+        const float m0 = m == -INFINITY ? 0.f : m, add = ve - m0;
+        if (!far) {
+          const uint64_t f2 = f2_pack(f, f), a2 = f2_pack(add, add);
+          uint64_t l0 = f2_pack(0.f, 0.f);
+          float r0 = 0.f, r1 = 0.f;  // of the rounded probabilities
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t s[32], p[16];
-          scores(c, s);
+          for (int c = 0; c < 2; ++c) {
+            uint32_t s[32], p[16];
+            scores(c, s);
 #pragma unroll
-          for (int q = 0; q < 16; ++q) {
-            float y0, y1;
-            f2_unpack(f2_fma(u2_pack(s[2 * q], s[2 * q + 1]), f2, a2), y0, y1);
-            y0 = fast_exp2(y0);
-            y1 = fast_exp2(y1);
-            l0 = f2_add(l0, f2_pack(y0, y1));
-            p[q] = pack2(y0, y1);
-            r0 = add_half(r0, (uint16_t)(p[q] & 0xffffu));
-            r1 = add_half(r1, (uint16_t)(p[q] >> 16));
+            for (int q = 0; q < 16; ++q) {
+              float y0, y1;
+              f2_unpack(f2_fma(u2_pack(s[2 * q], s[2 * q + 1]), f2, a2), y0, y1);
+              y0 = fast_exp2(y0);
+              y1 = fast_exp2(y1);
+              l0 = f2_add(l0, f2_pack(y0, y1));
+              p[q] = pack2(y0, y1);
+              r0 = add_half(r0, (uint16_t)(p[q] & 0xffffu));
+              r1 = add_half(r1, (uint16_t)(p[q] >> 16));
+            }
+            tmem_st16_async(ts + 16 * c, p);  // over scores that have been read
           }
-          tmem_st16_async(ts + 16 * c, p);  // over scores that have been read
+          float s0, s1;
+          f2_unpack(l0, s0, s1);
+          const float un = fast_exp2(kLift - ve);
+          l = fmaf(s0 + s1, un, l);
+          // (where all of a unit's p' are below 1, which is far below the largest: values of a small scale, whose p' may
+          // have lost bits that 2^-w makes matter, and whose weight in O is small)
+          lr = fmaf(unit_max < m ? s0 + s1 : r0 + r1, un, lr);
+        } else {
+          // (rare) l takes the weights themselves, as squares: 2^-149 where one exponential ends at 2^-126
+          float sum = 0.f;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t w = (uint32_t)(see >> (16 * c));
+            float s[16];
+            uint32_t p[8];
+            tmem_ld16(ts + 16 * c, s);
+#pragma unroll
+            for (int q = 0; q < 16; q += 2) {
+              float y[2];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const bool sees = w >> (q + k) & 1u;
+                const float x = s[q + k] * f;
+                const float h = sees ? fast_exp2(0.5f * (x - m0 + kLift)) : 0.f;
+                y[k] = sees ? fast_exp2(x + add) : 0.f;
+                sum = fmaf(h, h, sum);
+              }
+              p[q / 2] = pack2(y[0], y[1]);
+            }
+            tmem_st8_async(ts + 8 * c, p);  // over scores that have been read
+          }
+          l += sum;
+          lr += sum;
         }
-        float s0, s1;
-        f2_unpack(l0, s0, s1);
-        l = fmaf(s0 + s1, un, l);
-        // (where all of a unit's p' are below 1, which is far below the largest: values of a small scale, whose p' may
-        // have lost bits that 2^-w makes matter, and whose weight in O is small)
-        lr = fmaf(unit_max < m ? s0 + s1 : r0 + r1, un, lr);
         tmem_wait_st();
         tc_fence_before();
       }
@@ -802,8 +840,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
     const int node = row_ok ? by_g(qr) : 0;
     // normalised output of this stream; two streams of the same rows join in the first one.  It is written out, or
     // staged over operands that are done with (B_O follows every MMA) where a cluster shares the prefix.
-    float inv = !ok ? NAN : l == 0.f ? 0.f : 1.f / lr;
-    float lse = !ok ? NAN : l == 0.f ? -INFINITY : m + log2f(l);
+    // (2^kLift, and a quarter until the end: 448 * 2^120 is more than a float holds, a share of it may not be)
+    float inv = !ok ? NAN : l == 0.f ? 0.f : 1024.f / lr;
+    float lse = !ok ? NAN : l == 0.f ? -INFINITY : m - kLift + log2f(l);
     const bool o_on = ok && n_own > 0;  // (uniform: else O was never written)
     if (o_on) tc_fence_after();
     const uint32_t sw = (uint32_t)(r & 7) << 4;
@@ -878,7 +917,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
           uint4 w[4];
           T* e = reinterpret_cast<T*>(w);
 #pragma unroll
-          for (int q = 0; q < 32; ++q) e[q] = from_f32<T>(o[q]);
+          for (int q = 0; q < 32; ++q) e[q] = from_f32<T>(4.f * o[q]);
 #pragma unroll
           for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(smem + M::stage + r * 256 + (((4 * c + q) << 4) ^ sw)) = w[q];
         } else {
@@ -959,7 +998,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
       }
       T e[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = from_f32<T>(o[i]);
+      for (int i = 0; i < 8; ++i) e[i] = from_f32<T>(4.f * o[i]);
       if (mine) {
         T* const to = reinterpret_cast<T*>(a.out) + a.out_row_stride * (first + node) +
                       (size_t)(kvh * G + (q2 - node * G)) * kKv8Hd + 4 * l16;
