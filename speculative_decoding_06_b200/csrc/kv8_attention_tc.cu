@@ -33,8 +33,8 @@
 // 5 us), or read in half rows, a thread each (2000 cycles of the load pipe).
 //
 // Scales: the unit's K exponent (the largest of its pages'; codes of a page with a
-// smaller one are multiplied by the difference as they are converted, exact to
-// 2^-33 of the unit's largest value) multiplies the scores; its V exponent w goes
+// smaller one, by up to 2^kSpread, are multiplied by the difference as they are converted, which
+// is exact; further apart, each key keeps its page's) multiplies the scores; its V exponent w goes
 // into the exponential: p' = 2^(x + w - m) with m 7 below a running maximum of x + w,
 // moved only when exceeded by more than 15 (p' <= 2^15, and fp16 has its full 11 bits
 // down to 2^-21 of the largest p'), O sums p' times bare codes and the denominator
@@ -77,6 +77,8 @@ constexpr float kLift = 12.f;
 // Units whose w is that far below the largest so far may have p' = 0 for weights that count in l: l then takes the weights
 // themselves.  (A weight of 2^-43 of the largest has p' of 2^-126 or more at this distance.)
 constexpr float kFar = 90.f;
+// the smallest code is 2^-9 and fp16 ends at 2^-24
+constexpr int kSpread = 15;
 
 // mbarriers: per operand stage; S, P and P V per stream, for its even and its odd units: no wait is for a phase that
 // lies more than one behind what its waiter has seen, however far idle warps of a stream run ahead
@@ -98,7 +100,7 @@ struct M {  // shared memory
   static constexpr uint32_t group = codes + 2 * kCodeStages * kCodeTile;  // int4 [kMaxUnits]: first rows / 16 of the groups of 16 keys
   static constexpr uint32_t kexp = group + 16 * kMaxUnits;                // uint32 [kMaxUnits]: exponent bytes of the four groups
   static constexpr uint32_t vexp = kexp + 4 * kMaxUnits;
-  static constexpr uint32_t unit = vexp + 4 * kMaxUnits;  // float2 [kMaxUnits + 2]: factor of K, exponent of V
+  static constexpr uint32_t unit = vexp + 4 * kMaxUnits;  // float2 [kMaxUnits + 2]: factor of K (negative: each key has its own), exponent of V
   static constexpr uint32_t anc = unit + 8 * (kMaxUnits + 2);  // uint64 [2][128][2]
   static constexpr uint32_t jump = anc + 2 * 128 * 16;    // int [2][128]
   static constexpr uint32_t half = jump + 2 * 128 * 4;    // float [2][128]: largest values of the halves of q, at the end the streams' log-sum-exps
@@ -153,6 +155,9 @@ __device__ __forceinline__ float scale_of(int byte) { return byte >= 255 ? NAN :
 __device__ __forceinline__ float exp_of(int byte) { return byte >= 255 ? NAN : (float)(byte - 127); }
 __device__ __forceinline__ int max4(uint32_t w) {
   return max(max((int)(w & 255), (int)(w >> 8 & 255)), max((int)(w >> 16 & 255), (int)(w >> 24)));
+}
+__device__ __forceinline__ int min4(uint32_t w) {
+  return min(min((int)(w & 255), (int)(w >> 8 & 255)), min((int)(w >> 16 & 255), (int)(w >> 24)));
 }
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
@@ -358,14 +363,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
       if (i < np) {
         uint32_t ke = bad, ve = 0;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const bool none = c0 + kKeys * i + 16 * u >= c1;
-          ke |= (none ? 0u : (uint32_t)c.exps[0][at[u]]) << (8 * u);
-          ve |= (none ? 0u : (uint32_t)c.exps[1][at[u]]) << (8 * u);
+        for (int u = 0; u < 4; ++u) {  // (groups behind the end have the first one's)
+          const int from = c0 + kKeys * i + 16 * u >= c1 ? at[0] : at[u];
+          ke |= (uint32_t)c.exps[0][from] << (8 * u);
+          ve |= (uint32_t)c.exps[1][from] << (8 * u);
         }
         reinterpret_cast<uint32_t*>(smem + M::kexp)[i] = ke;
         reinterpret_cast<uint32_t*>(smem + M::vexp)[i] = ve;
-        s_unit[i] = make_float2(scale_of(max4(ke)), exp_of(max4(ve)));
+        const int k_top = max4(ke), v_top = max4(ve);
+        const bool keyed = max(k_top - min4(ke), v_top - min4(ve)) > kSpread;
+        s_unit[i] = make_float2(keyed ? -scale_of(k_top) : scale_of(k_top), exp_of(v_top));
       }
     }
   }
@@ -529,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
       const uint32_t e4 = s_exp[j];
       uint8_t* const op = enter();
       if (!ok) break;
-      if (e4 == __byte_perm(e4, 0, 0)) {  // pages of one scale
+      if (e4 == __byte_perm(e4, 0, 0) || s_unit[j].x < 0.f) {  // pages of one scale, or codes as they are
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           uint4 lo, hi;
@@ -545,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
 #pragma unroll 1
         for (int u = 0; u < 4; ++u) {
           const int d = ref - (int)(e4 >> (8 * u) & 255);
-          const __half2 f = __float2half2_rn(d > 24 ? 0.f : pow2i(-d));
+          const __half2 f = __float2half2_rn(pow2i(-d));
           const uint4 y = u == 0 ? w[0] : u == 1 ? w[1] : u == 2 ? w[2] : w[3];
           uint4 lo, hi;
           expand4(y.x, lo.x, lo.y);
@@ -708,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
       }
       const float2 e = s_unit[u];
       const float f = qs * e.x, ve = e.y;
-      const bool far = ve < top_w - kFar;  // (of all threads alike)
+      const bool keyed = e.x < 0.f, apart = keyed || ve < top_w - kFar;  // (of all threads alike)
       top_w = fmaxf(top_w, ve);
       if (ok) ok = held(B_SFULL + eo, ph);
       ok = __all_sync(0xffffffffu, ok);
@@ -726,20 +733,40 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
             for (int q = 0; q < 32; ++q) s[q] = (w >> q & 1u) ? s[q] : 0xff800000u;
           }
         };
-        float mx = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t s[32];
-          scores(c, s);
-          float m0 = __uint_as_float(s[0]), m1 = __uint_as_float(s[1]);
-#pragma unroll
-          for (int q = 2; q < 30; q += 4) {
-            m0 = fmax3(m0, __uint_as_float(s[q]), __uint_as_float(s[q + 1]));
-            m1 = fmax3(m1, __uint_as_float(s[q + 2]), __uint_as_float(s[q + 3]));
+        // of keys 16 c .. of a unit with scales of its own: K's factor and V's exponent
+        auto of_keys = [&](int c, float& kf, float& kv) {
+          kf = f, kv = ve;
+          if (keyed) {
+            kf = qs * scale_of(reinterpret_cast<const uint32_t*>(smem + M::kexp)[u] >> (8 * c) & 255);
+            kv = exp_of(reinterpret_cast<const uint32_t*>(smem + M::vexp)[u] >> (8 * c) & 255);
           }
-          mx = fmax3(mx, fmax3(m0, __uint_as_float(s[30]), __uint_as_float(s[31])), m1);
+        };
+        float mx = -INFINITY;
+        if (keyed) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            float s[16], kf, kv;
+            tmem_ld16(ts + 16 * c, s);
+            of_keys(c, kf, kv);
+            const uint32_t w = (uint32_t)(see >> (16 * c));
+#pragma unroll
+            for (int q = 0; q < 16; ++q) mx = fmaxf(mx, w >> q & 1u ? fmaf(s[q], kf, kv) : -INFINITY);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t s[32];
+            scores(c, s);
+            float m0 = __uint_as_float(s[0]), m1 = __uint_as_float(s[1]);
+#pragma unroll
+            for (int q = 2; q < 30; q += 4) {
+              m0 = fmax3(m0, __uint_as_float(s[q]), __uint_as_float(s[q + 1]));
+              m1 = fmax3(m1, __uint_as_float(s[q + 2]), __uint_as_float(s[q + 3]));
+            }
+            mx = fmax3(mx, fmax3(m0, __uint_as_float(s[30]), __uint_as_float(s[31])), m1);
+          }
+          mx = fmaf(mx, f, ve);
         }
-        mx = fmaf(mx, f, ve);
         const float unit_max = mx;
         const bool up = mx > m + 15.f;
         if (__any_sync(0xffffffffu, up)) {
@@ -766,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
           }
         }
         const float m0 = m == -INFINITY ? 0.f : m, add = ve - m0;
-        if (!far) {
+        if (!apart) {
           const uint64_t f2 = f2_pack(f, f), a2 = f2_pack(add, add);
           uint64_t l0 = f2_pack(0.f, 0.f);
           float r0 = 0.f, r1 = 0.f;  // of the rounded probabilities
@@ -800,18 +827,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             const uint32_t w = (uint32_t)(see >> (16 * c));
-            float s[16];
+            float s[16], kf, kv;
             uint32_t p[8];
             tmem_ld16(ts + 16 * c, s);
+            of_keys(c, kf, kv);
 #pragma unroll
             for (int q = 0; q < 16; q += 2) {
               float y[2];
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
                 const bool sees = w >> (q + k) & 1u;
-                const float x = s[q + k] * f;
-                const float h = sees ? fast_exp2(0.5f * (x - m0 + kLift)) : 0.f;
-                y[k] = sees ? fast_exp2(x + add) : 0.f;
+                const float x = s[q + k] * kf - m0;
+                const float h = sees ? fast_exp2(0.5f * (x + kLift)) : 0.f;
+                y[k] = sees ? fast_exp2(x + kv) : 0.f;
                 sum = fmaf(h, h, sum);
               }
               p[q / 2] = pack2(y[0], y[1]);

@@ -20,26 +20,85 @@ def set_exps(c, plane, table):
     c["cache"].exps[0] = torch.from_numpy(c["exps"])
 
 
+def infinite_beyond_the_type(out, ref):
+    """448 * 2^120 is above the largest bf16, 2^128 (1 - 2^-8): rounding to nearest gives that one up to 2^128 (1 - 2^-9)
+    and infinity from there on.  A value beyond this border by more than its bound has to be infinite, one that the bound
+    lets lie on either side may be; both are taken out of what is compared."""
+    got, edge = out.double().cpu().numpy(), 2.0 ** 128 * (1 - 2.0 ** -9)
+    off = (2.0 ** -8 + 2.0 ** -11 + 2 * 130 * 2.0 ** -24 * ref[3] + 2.0 ** -18)[..., None] * ref[2]  # before the last rounding
+    inf = np.isinf(got) & (np.sign(got) == np.sign(ref[0])) & (np.abs(ref[0]) + off >= edge)
+    assert inf[np.abs(ref[0]) - off > edge].all()
+    out[torch.from_numpy(inf).cuda()], ref[0][inf] = 0, 0
+
+
 @pytest.mark.parametrize("high", [150, 190, 247])
-@pytest.mark.parametrize("order", ["small first", "large first", "in turn"])
+@pytest.mark.parametrize("order", ["small first", "large first", "in turn", "page by page"])
 @pytest.mark.parametrize("prefixes,nodes,hq,page,dtype", [
     ([200, 77], [1, 1], 4, 16, "bf16"), ([3000], [1], 4, 64, "bf16"), ([900, 130], [3, 2], 4, 32, "bf16"),
-    ([300, 190], [30, 100], 4, 64, "bf16"), ([3000], [40], 8, 64, "bf16"), ([500], [17], 2, 128, "bf16")])
+    ([300, 190], [30, 100], 4, 64, "bf16"), ([3000], [40], 8, 64, "bf16"), ([500], [17], 2, 128, "bf16"),
+    ([300, 61], [30, 100], 4, 16, "bf16"), ([1000], [40], 4, 32, "bf16")])
 def test_weights_of_pages_whose_values_are_of_unlike_size(prefixes, nodes, hq, page, dtype, order, high):
     """V pages at the least scale (all zeros have it) beside very large ones: the weights do not depend on V."""
     c = attention_case(31, prefixes, nodes, hq, 1, page, dtype)
     blocks = [-(-p // page) for p in prefixes]
     # (in turn: no two scales within 64 keys)
     large = {"small first": lambda b, j: 2 * j >= blocks[b], "large first": lambda b, j: 2 * j < blocks[b],
-             "in turn": lambda b, j: j * page // 64 % 2 == 1}[order]
-    if page < 64:  # whole units of 64 keys
+             "in turn": lambda b, j: j * page // 64 % 2 == 1, "page by page": lambda b, j: j % 2 == 1}[order]
+    if page < 64 and order != "page by page":  # whole units of 64 keys
         was = large
         large = lambda b, j: was(b, j // (64 // page) * (64 // page))  # noqa: E731
     set_exps(c, 1, lambda b, j: high if large(b, j) else 67)
-    # (448 * 2^120 is above the largest bf16, 1.99 * 2^127: an average above it is an infinity in bf16)
     (out, lse), ref = run_attention(c), reference(c)
-    over = np.abs(ref[0]) > torch.finfo(out.dtype).max
-    at = torch.from_numpy(over).cuda()
-    assert np.array_equal(out[at].double().cpu().numpy(), np.sign(ref[0][over]) * np.inf)
-    out[at], ref[0][over] = 0, 0
+    infinite_beyond_the_type(out, ref)
     check_attention(c, (out, lse), ref)
+
+
+def drop_pages(c, keep):
+    """The same sequences without the pages for which keep(b, j) is false (their weights are below 2^-60)."""
+    r = dict(c, tables=c["tables"].copy(), lengths=c["lengths"].copy())
+    for b, s in enumerate(c["ids"]):
+        P, page = int(c["lengths"][s]), c["page"]
+        used = [j for j in range(-(-P // page)) if keep(b, j)]
+        r["tables"][s, :len(used)] = c["tables"][s, used]
+        r["lengths"][s] = sum(min(page, P - page * j) for j in used)
+    return r
+
+
+# prefixes of whole pages but for the last, which is kept
+MIXED = [([64], [1], 4, 16, "bf16"), ([150, 64], [1, 3], 4, 16, "fp16"), ([150, 64], [30, 100], 4, 16, "bf16"),
+         ([128, 331], [20, 17], 2, 32, "fp16"), ([1000], [40], 4, 16, "bf16")]
+
+
+@pytest.mark.parametrize("gap", [9, 15, 16, 23, 25, 30, 60])
+@pytest.mark.parametrize("prefixes,nodes,hq,page,dtype", MIXED)
+def test_values_of_a_small_page_that_has_the_weight(prefixes, nodes, hq, page, dtype, gap):
+    """Every other page holds V that is 2^gap larger, at keys whose scores are some 95 powers of two lower."""
+    c = attention_case(32, prefixes, nodes, hq, 1, page, dtype, tree="none")
+    keep = lambda b, j: j % 2 == (-(-prefixes[b] // page) - 1) % 2  # noqa: E731  (the last page is a small one)
+    set_exps(c, 0, lambda b, j: 127 - 8)
+    set_exps(c, 1, lambda b, j: 127 - 8 + (0 if keep(b, j) else gap))
+    for b, s in enumerate(c["ids"]):
+        for j in range(-(-prefixes[b] // page)):
+            c["codes"][0, c["tables"][s, j], :, :, 0] = 0x77 if keep(b, j) else 0xF7  # K's first dimension: 240 or -240
+    c["cache"].codes[0] = torch.from_numpy(c["codes"])
+    c["q"][..., 0] = 400.0
+    check_attention(c, run_attention(c), reference(drop_pages(c, keep)))
+
+
+@pytest.mark.parametrize("gap", [9, 15, 16, 23, 25, 30, 60])
+@pytest.mark.parametrize("prefixes,nodes,hq,page,dtype", MIXED)
+def test_keys_of_a_small_page_beside_large_ones(prefixes, nodes, hq, page, dtype, gap):
+    """Every other page holds K that is 2^gap larger, all of its scores far below the others'."""
+    c = attention_case(33, prefixes, nodes, hq, 1, page, dtype, tree="none")
+    keep = lambda b, j: j % 2 == (-(-prefixes[b] // page) - 1) % 2  # noqa: E731
+    set_exps(c, 0, lambda b, j: 127 - 8 + (0 if keep(b, j) else gap))
+    set_exps(c, 1, lambda b, j: 127 - 8)
+    for b, s in enumerate(c["ids"]):
+        for j in range(-(-prefixes[b] // page)):
+            if not keep(b, j):
+                c["codes"][0, c["tables"][s, j]] = 0
+                c["codes"][0, c["tables"][s, j], :, :, 0] = 0xF7
+    c["codes"][0, :, :, :, 0] = np.where(c["codes"][0, :, :, :, 0] == 0xF7, 0xF7, 0)  # else 0 where q is large
+    c["cache"].codes[0] = torch.from_numpy(c["codes"])
+    c["q"][..., 0] = 400.0
+    check_attention(c, run_attention(c), reference(drop_pages(c, keep)))
