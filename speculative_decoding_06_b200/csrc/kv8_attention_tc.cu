@@ -12,7 +12,8 @@
 //   helper (1 warp)       the tree's ancestor sets.
 //   converters (4 warps for K, 4 for V)  turn codes into fp16 (exact) and write them as
 //       the swizzled K and V operands.  K and V of the step's own rows become fp16
-//       times a power of two that their largest value sets.
+//       times a power of two that the largest value of 64 rows sets, or, where their sizes differ
+//       by more than 2^kRowSpread, each row's own: a row must not suffer from one that it does not see.
 //   issuers (1 thread per stream)  S = Q K^T (M 128, N 64) with q in TMEM, into one of three
 //       TMEM buffers, and O += P V (P from TMEM, V MN-major); scores run a unit ahead of products.
 //   softmax (4 warps per stream)  a thread per row: the online softmax in base 2, P as
@@ -79,6 +80,8 @@ constexpr float kLift = 12.f;
 constexpr float kFar = 90.f;
 // the smallest code is 2^-9 and fp16 ends at 2^-24
 constexpr int kSpread = 15;
+// (fp16 has its 11 bits down to 2^-21 of a tile's largest value: 2^-13 of the largest of a row that is 2^-8 as large)
+constexpr int kRowSpread = 8;
 
 // mbarriers: per operand stage; S, P and P V per stream, for its even and its odd units: no wait is for a phase that
 // lies more than one behind what its waiter has seen, however far idle warps of a stream run ahead
@@ -104,9 +107,9 @@ struct M {  // shared memory
   static constexpr uint32_t anc = unit + 8 * (kMaxUnits + 2);  // uint64 [2][128][2]
   static constexpr uint32_t jump = anc + 2 * 128 * 16;    // int [2][128]
   static constexpr uint32_t half = jump + 2 * 128 * 4;    // float [2][128]: largest values of the halves of q, at the end the streams' log-sum-exps
-  static constexpr uint32_t row = half + 2 * 128 * 4;     // float [256]: at the end the rows' log-sum-exps
-  static constexpr uint32_t red = row + 2 * 128 * 4;      // float [8]: the converter warps' largest K and V values
-  static constexpr uint32_t vbad = red + 32;              // uint32 [4]: own rows whose V holds an infinity or NaN
+  static constexpr uint32_t row = half + 2 * 128 * 4;     // uint32 [2][2][64]: the largest values of halves of 64 own rows of K and V; at the end float [128]: the rows' log-sum-exps
+  static constexpr uint32_t own = row + 2 * 128 * 4;      // uint8 [2][128]: exponent bytes of the own rows of K and V
+  static constexpr uint32_t vbad = own + 256;             // uint32 [4]: own rows whose V holds an infinity or NaN
   static constexpr uint32_t bars = vbad + 16;
   static constexpr uint32_t misc = bars + 8 * kNumBars + 8;
   static constexpr uint32_t end = misc + 16;
@@ -208,11 +211,62 @@ __device__ __forceinline__ bool finite_only(uint4& r) {
   return any;
 }
 
+// Each thread of the warp reads 4, writes 2 consecutive 32-bit columns of its own lane.
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, float (&v)[4]) {
+  uint32_t r[4];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st2_async(uint32_t taddr, uint32_t a, uint32_t b) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1,%2};" ::"r"(taddr), "r"(a), "r"(b) : "memory");
+}
+
 // a + c, a in 16 bits
 __device__ __forceinline__ float add_half(float c, uint16_t a) {
   float d;
   asm("add.f32.f16 %0, %1, %2;" : "=f"(d) : "h"(a), "f"(c));
   return d;
+}
+
+// A unit whose keys have exponents of their own, or whose weights p' may not hold, in tensor memory at `ts` (rare, and so
+// kept out of the loop that calls it).  P false: the largest x + w.  P true: writes p' over the scores and returns the sum
+// of the weights 2^(x - m + kLift), taken as squares: these end at 2^-149 where one exponential ends at 2^-126.
+// bytes: K's exponent bytes, V's behind them; null: f is K's whole factor and ve V's exponent.
+template <bool P>
+__device__ __noinline__ float unit_apart(uint32_t ts, uint64_t see, const uint8_t* bytes, bool pages, float f, float ve,
+                                         float m) {
+  float r = P ? 0.f : -INFINITY;
+#pragma unroll 1
+  for (int j = 0; j < kKeys / 4; ++j) {
+    float x[4], w[4];
+    tmem_ld4(ts + 4 * j, x);
+    const uint32_t sees = (uint32_t)(see >> (4 * j));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      w[k] = ve;
+      float kf = f;
+      if (bytes) {
+        const uint8_t* at = bytes + (pages ? j >> 2 : 4 * j + k);
+        kf *= scale_of(*at);
+        w[k] = exp_of(at[pages ? M::vexp - M::kexp : 128]);
+      }
+      x[k] = sees >> k & 1u ? x[k] * kf : -INFINITY;
+      if (P) {
+        const float h = fast_exp2(0.5f * (x[k] - m + kLift));
+        r = fmaf(h, h, r);
+        x[k] = fast_exp2(x[k] + (w[k] - m));
+      } else {
+        r = fmaxf(r, x[k] + w[k]);
+      }
+    }
+    if (P) tmem_st2_async(ts + 2 * j, pack2(x[0], x[1]), pack2(x[2], x[3]));  // over scores that have been read
+  }
+  return r;
 }
 
 template <typename T>
@@ -505,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
       if (++st == n_stages) st = 0, ph ^= 1;
     };
     const uint32_t* const s_exp = reinterpret_cast<const uint32_t*>(smem + (p ? M::vexp : M::kexp));
-    // the step's own rows, 64 nodes per tile: their largest finite value sets the tile's exponent.  They are looked at
+    // the step's own rows, 64 nodes per tile: their largest finite values set the exponents.  They are looked at
     // last, while the prefix's last units wait for their turn
     const T* const own = reinterpret_cast<const T*>(p ? a.v_new : a.k_new) +
                          (p ? a.v_head_stride : a.k_head_stride) * kvh + 16 * ch;
@@ -574,34 +628,65 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
       uint4 raw[4][2];
 #pragma unroll
       for (int u = 0; u < 4; ++u) own_row(tt, u, raw[u]);
-      uint32_t big = 0;
+      uint32_t big[4];  // of the thread's half pieces of four rows, then of the warp's
+      uint32_t wild = 0;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const uint4 r = raw[u >> 1][u & 1];
-        big = max_abs_nan<T>(max_abs_nan<T>(max_abs_nan<T>(max_abs_nan<T>(big, r.x), r.y), r.z), r.w);
+      for (int u = 0; u < 4; ++u) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const uint4 r = raw[u][hh];
+          m = max_abs_nan<T>(max_abs_nan<T>(max_abs_nan<T>(max_abs_nan<T>(m, r.x), r.y), r.z), r.w);
+        }
+        big[u] = max(m & 0xffffu, m >> 16);
+        wild |= big[u] >= inf_bits<T>() ? 1u << u : 0u;
       }
-      if (max(big & 0xffffu, big >> 16) >= inf_bits<T>()) {  // (rare) infinities or NaN
-        big = 0;
+      if (wild) {  // (rare) infinities or NaN
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          bool wild = false;
+          if (!(wild >> u & 1u)) continue;
+          uint32_t m = 0;
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) wild |= finite_only<T>(raw[u][hh]);
-          big = max_abs2(max_abs2(max_abs2(max_abs2(big, raw[u][0].x), raw[u][0].y), raw[u][0].z), raw[u][0].w);
-          big = max_abs2(max_abs2(max_abs2(max_abs2(big, raw[u][1].x), raw[u][1].y), raw[u][1].z), raw[u][1].w);
+          for (int hh = 0; hh < 2; ++hh) {
+            finite_only<T>(raw[u][hh]);
+            m = max_abs2(max_abs2(max_abs2(max_abs2(m, raw[u][hh].x), raw[u][hh].y), raw[u][hh].z), raw[u][hh].w);
+          }
+          big[u] = max(m & 0xffffu, m >> 16);
           const int node = kKeys * tt + 16 * u + kr;
-          if (p && wild) atomicOr(&s_vbad[node >> 5], 1u << (node & 31));
+          if (p) atomicOr(&s_vbad[node >> 5], 1u << (node & 31));
         }
       }
-      big = __reduce_max_sync(0xffffffffu, max(big & 0xffffu, big >> 16));
-      uint32_t* red = reinterpret_cast<uint32_t*>(smem + M::red) + kConvWarps * p;
-      if (lane == 0) red[x >> 5] = big;
-      sync_converters(p);
+      // four lanes have pieces of a row in this warp, four more in its neighbour
+      uint32_t* const red = reinterpret_cast<uint32_t*>(smem + M::row) + 128 * p;
 #pragma unroll
-      for (int w = 0; w < kConvWarps; ++w) big = max(big, red[w]);
-      const uint16_t top_bits = (uint16_t)big;
-      const int shift = shift_of(to_f32<T>(*reinterpret_cast<const T*>(&top_bits)), p ? -80 : -100);
-      if (x == 0) (&s_unit[np + tt].x)[p] = p ? (float)shift : pow2i(shift);
+      for (int u = 0; u < 4; ++u) {
+        big[u] = max(big[u], __shfl_xor_sync(0xffffffffu, big[u], 8));
+        big[u] = max(big[u], __shfl_xor_sync(0xffffffffu, big[u], 16));
+        if (lane < 8) red[64 * (wv & 1) + 16 * u + kr] = big[u];
+      }
+      sync_converters(p);
+      // (every warp alike) the rows' exponents; rows of zeros take the tile's
+      int e[2], most = -1000, least = 1000;
+      bool zero[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint16_t bits = (uint16_t)max(red[lane + 32 * k], red[64 + lane + 32 * k]);
+        e[k] = shift_of(to_f32<T>(*reinterpret_cast<const T*>(&bits)), p ? -80 : -100);
+        zero[k] = bits == 0;
+        most = zero[k] ? most : max(most, e[k]);
+        least = zero[k] ? least : min(least, e[k]);
+      }
+      most = __reduce_max_sync(0xffffffffu, most);
+      least = __reduce_min_sync(0xffffffffu, least);
+      if (most == -1000) most = 0;
+      const bool keyed = most - least > kRowSpread;
+      if (wv == 0) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          smem[M::own + 128 * p + kKeys * tt + lane + 32 * k] = (uint8_t)(127 + (keyed && !zero[k] ? e[k] : most));
+        // (K's sign, V's 1024: the keys have exponents of their own)
+        if (lane == 0) (&s_unit[np + tt].x)[p] = p ? (float)(keyed ? most + 1024 : most) : keyed ? -pow2i(most) : pow2i(most);
+      }
       sync_converters(p);  // (also: everyone has read `red`)
       if (lane == 0) mbar_arrive(&bar[B_TREF + tt]);
     }
@@ -609,8 +694,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
       const int j = np + tt;
       uint8_t* const op = enter();
       if (!ok) break;
-      const float2 e = s_unit[j];
-      const float f = p ? pow2i(-(int)e.y) : 1.f / e.x;  // (powers of two)
       // V's infinities and NaN become 0, because 0 * NaN would reach rows that do not see them; they are added at
       // the end
       const bool wild = p && (s_vbad[2 * tt] | s_vbad[2 * tt + 1]);
@@ -618,6 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
       for (int u = 0; u < 4; ++u) {
         uint4 raw[2];
         own_row(tt, u, raw);
+        const float f = pow2i(127 - (int)smem[M::own + 128 * p + kKeys * tt + 16 * u + kr]);
         if (wild) {
           finite_only<T>(raw[0]);
           finite_only<T>(raw[1]);
@@ -693,13 +777,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
     }
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);  // this warp's lanes
     const uint32_t to = tl + 128 * t;                                 // the stream's O
-    int sb = t, eo = 2 * t, ph = 0;                                   // the unit's S buffer, barrier and phase
+    int sb = t;                                                       // the unit's S buffer
     const int n_own = (nu - t + 1) >> 1;  // the stream's units
     float m = -INFINITY, l = 0.f, lr = 0.f;  // lr: of the rounded probabilities
     float top_w = -INFINITY;                 // the largest w so far
 #pragma unroll 1
     for (int i = 0; i < n_own; ++i) {
-      const int u = 2 * i + t;
+      const int u = 2 * i + t, eo = 2 * t + (i & 1), ph = (i >> 1) & 1;  // its barrier and phase
       const uint32_t ts = tl + kColS + kKeys * sb;
       uint64_t see = ~0ull;  // keys of the unit that the row sees
       if (u >= np - 1) {
@@ -715,12 +799,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
       }
       const float2 e = s_unit[u];
       const float f = qs * e.x, ve = e.y;
-      const bool keyed = e.x < 0.f, apart = keyed || ve < top_w - kFar;  // (of all threads alike)
-      top_w = fmaxf(top_w, ve);
       if (ok) ok = held(B_SFULL + eo, ph);
       ok = __all_sync(0xffffffffu, ok);
       if (ok && warp_on) {
         tc_fence_after();
+        const bool keyed = e.x < 0.f || ve > 512.f;  // (of all threads alike, `apart` too)
+        const bool apart = keyed || ve < top_w - kFar;
+        top_w = fmaxf(top_w, ve > 512.f ? ve - 1024.f : ve);
         // twice through the scores, 32 at a time: the largest first
         const bool masked = __any_sync(0xffffffffu, see != ~0ull);
         auto scores = [&](int c, uint32_t (&s)[32]) {
@@ -733,25 +818,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
             for (int q = 0; q < 32; ++q) s[q] = (w >> q & 1u) ? s[q] : 0xff800000u;
           }
         };
-        // of keys 16 c .. of a unit with scales of its own: K's factor and V's exponent
-        auto of_keys = [&](int c, float& kf, float& kv) {
-          kf = f, kv = ve;
-          if (keyed) {
-            kf = qs * scale_of(reinterpret_cast<const uint32_t*>(smem + M::kexp)[u] >> (8 * c) & 255);
-            kv = exp_of(reinterpret_cast<const uint32_t*>(smem + M::vexp)[u] >> (8 * c) & 255);
-          }
-        };
+        // exponent bytes of the unit's K, one per 16 keys or per own row; those of V lie as far behind as their arrays
+        const uint8_t* const bytes = !keyed ? nullptr : smem + (u < np ? M::kexp + 4 * u : M::own + kKeys * (u - np));
         float mx = -INFINITY;
-        if (keyed) {
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            float s[16], kf, kv;
-            tmem_ld16(ts + 16 * c, s);
-            of_keys(c, kf, kv);
-            const uint32_t w = (uint32_t)(see >> (16 * c));
-#pragma unroll
-            for (int q = 0; q < 16; ++q) mx = fmaxf(mx, w >> q & 1u ? fmaf(s[q], kf, kv) : -INFINITY);
-          }
+        if (__builtin_expect(keyed, 0)) {
+          mx = unit_apart<false>(ts, see, bytes, u < np, qs, ve, 0.f);
         } else {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
@@ -793,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
           }
         }
         const float m0 = m == -INFINITY ? 0.f : m, add = ve - m0;
-        if (!apart) {
+        if (__builtin_expect(!apart, 1)) {
           const uint64_t f2 = f2_pack(f, f), a2 = f2_pack(add, add);
           uint64_t l0 = f2_pack(0.f, 0.f);
           float r0 = 0.f, r1 = 0.f;  // of the rounded probabilities
@@ -822,30 +893,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
           // have lost bits that 2^-w makes matter, and whose weight in O is small)
           lr = fmaf(unit_max < m ? s0 + s1 : r0 + r1, un, lr);
         } else {
-          // (rare) l takes the weights themselves, as squares: 2^-149 where one exponential ends at 2^-126
-          float sum = 0.f;
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t w = (uint32_t)(see >> (16 * c));
-            float s[16], kf, kv;
-            uint32_t p[8];
-            tmem_ld16(ts + 16 * c, s);
-            of_keys(c, kf, kv);
-#pragma unroll
-            for (int q = 0; q < 16; q += 2) {
-              float y[2];
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const bool sees = w >> (q + k) & 1u;
-                const float x = s[q + k] * kf - m0;
-                const float h = sees ? fast_exp2(0.5f * (x + kLift)) : 0.f;
-                y[k] = sees ? fast_exp2(x + kv) : 0.f;
-                sum = fmaf(h, h, sum);
-              }
-              p[q / 2] = pack2(y[0], y[1]);
-            }
-            tmem_st8_async(ts + 8 * c, p);  // over scores that have been read
-          }
+          const float sum = unit_apart<true>(ts, see, bytes, u < np, keyed ? qs : f, ve, m0);
           l += sum;
           lr += sum;
         }
@@ -854,8 +902,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar[B_PFULL + eo]);
-      ph ^= eo & 1;
-      eo ^= 1;
       if ((sb += 2) >= kScores) sb -= kScores;
     }
     if (ok && nu > 0) ok = held(B_O, 0);

@@ -102,3 +102,40 @@ def test_keys_of_a_small_page_beside_large_ones(prefixes, nodes, hq, page, dtype
     c["cache"].codes[0] = torch.from_numpy(c["codes"])
     c["q"][..., 0] = 400.0
     check_attention(c, run_attention(c), reference(drop_pages(c, keep)))
+
+
+@pytest.mark.parametrize("which", ["k", "v", "both"])
+@pytest.mark.parametrize("size", [2.0 ** 13, 1e9, 1e30])
+@pytest.mark.parametrize("prefixes,nodes,hq", [([70], [4], 4), ([70, 0], [61, 20], 4), ([33], [128], 2), ([0], [17], 2)])
+def test_large_rows_reach_only_the_rows_that_see_them(prefixes, nodes, hq, size, which):
+    """One of the step's own rows, which no other row sees, is very large but finite: the others' results stay."""
+    c = attention_case(34, prefixes, nodes, hq, 1, 32, "bf16")
+    off, big = c["offsets"], []
+    for b, n in enumerate(nodes):
+        for leaf in (1, n - 1):  # no row's parent any more
+            at = off[b] + leaf
+            for j in range(off[b], off[b + 1]):
+                if c["parents"][j] == leaf:
+                    c["parents"][j] = 0
+            big.append(at)
+    fine = np.ones(sum(nodes), bool)
+    fine[big] = False
+    ref = reference(c)  # (the rows that do not see them have the same result without)
+    for at in big:
+        for name in ("k", "v"):
+            if which in (name, "both"):
+                c[name][at] = (c[name][at].float() * size).to(c[name].dtype)
+    out, lse = run_attention(c)
+    rows = torch.from_numpy(fine).cuda()
+    check_attention(c, (out[rows], lse[rows]), [x[fine] for x in ref])
+    assert not torch.isnan(out).any() and not torch.isnan(lse).any()
+
+
+@pytest.mark.parametrize("nodes", [[3], [61], [128]])
+def test_rows_of_every_size(nodes):
+    """K and V of each node of its own size, 2^-40 to 2^40: every row is right to within its own weights."""
+    c = attention_case(35, [90], nodes, 4, 1, 64, "bf16")
+    g = np.random.default_rng(5)
+    c["v"] = (c["v"].float() * torch.exp2(torch.from_numpy(g.integers(-40, 41, (nodes[0], 1, 1)))).float()).to(torch.bfloat16)
+    c["k"] = (c["k"].float() * torch.exp2(torch.from_numpy(g.integers(-40, 1, (nodes[0], 1, 1)))).float()).to(torch.bfloat16)
+    check_attention(c, run_attention(c), reference(c))
