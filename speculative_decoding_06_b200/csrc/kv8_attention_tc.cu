@@ -798,7 +798,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
         }
       }
       const float2 e = s_unit[u];
-      const float f = qs * e.x, ve = e.y;
+      // (a factor that vanishes would turn hidden keys' -inf into NaN)
+      const float f = fabsf(qs * e.x) < 0x1p-126f ? 0x1p-126f : qs * e.x, ve = e.y;
       if (ok) ok = held(B_SFULL + eo, ph);
       ok = __all_sync(0xffffffffu, ok);
       if (ok && warp_on) {

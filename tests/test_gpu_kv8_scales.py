@@ -139,3 +139,14 @@ def test_rows_of_every_size(nodes):
     c["v"] = (c["v"].float() * torch.exp2(torch.from_numpy(g.integers(-40, 41, (nodes[0], 1, 1)))).float()).to(torch.bfloat16)
     c["k"] = (c["k"].float() * torch.exp2(torch.from_numpy(g.integers(-40, 1, (nodes[0], 1, 1)))).float()).to(torch.bfloat16)
     check_attention(c, run_attention(c), reference(c))
+
+
+@pytest.mark.parametrize("prefixes,nodes,tree", [([70, 5], [2, 1], "tree"), ([70, 5], [61, 20], "tree"),
+                                                 ([70, 3], [40, 33], "none"), ([0], [100], "chain")])
+def test_scores_that_vanish(prefixes, nodes, tree):
+    """q near 2^-100 and keys of the least scale: every score is 0, what a row does not see stays out of it."""
+    c = attention_case(36, prefixes, nodes, 4, 1, 16, "bf16", tree)
+    c["q"] = (c["q"].float() * 2.0 ** -100).to(torch.bfloat16)
+    set_exps(c, 0, lambda b, j: 67)
+    check_attention(c, run_attention(c), reference(c))
+    check_attention(c, run_attention(c, scale=1e-38), reference(c, 1e-38))
