@@ -509,8 +509,9 @@ SPEC_API int spec_kv8_append(spec_kv8* h, int layer, const spec_kv8_append_args*
  *   out[row][h] = sum_j softmax_j(scale q.k_j) v_j,  lse[row][h] = ln sum_j exp(scale q.k_j)
  * A row that sees nothing gets out 0 and lse -inf.  Rows beyond offsets[batch] are
  * left as they were, as are those of an entry whose sequence id, length, row count
- * (1 .. max_nodes) or offsets are out of range; a page id outside the cache reads
- * as NaN.  out may not overlap the inputs.  Infinities and NaN in q, k_new and v_new
+ * (1 .. max_nodes) or offsets are out of range; with `fill`, for buffers that hold
+ * nothing yet, the former get what a row gets that sees nothing, the latter NaN.  A
+ * page id outside the cache reads as NaN.  out may not overlap the inputs.  Infinities and NaN in q, k_new and v_new
  * reach only the rows that see them, whatever lies in the cache behind a sequence's
  * end none. */
 typedef struct spec_kv8_attention_args {
@@ -539,7 +540,10 @@ typedef struct spec_kv8_attention_args {
   int32_t max_nodes;       /* most rows of one entry: 1 .. 128 */
   int32_t max_prefix;      /* no lengths[s] is above this (entries above it are left as they were) */
   float scale;             /* > 0; 0: 1 / sqrt(128) */
+  int32_t fill;            /* SPEC_KV8_FILL_*: rows of no entry, or of one out of range, are written too */
 } spec_kv8_attention_args;
+#define SPEC_KV8_FILL_OUT 1
+#define SPEC_KV8_FILL_LSE 2
 #define SPEC_KV8_WORKSPACE_ZERO 65536
 /* Workspace bytes of spec_kv8_attention for these bounds and for all calls whose bounds are none of them above these:
  * a program makes one workspace for its largest batch, trees and prefixes (0: bounds rejected). */

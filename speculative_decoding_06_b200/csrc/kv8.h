@@ -43,4 +43,34 @@ cudaError_t launch_kv8_attention(const Kv8View& c, const CUtensorMap& map, const
 cudaError_t kv8_tree_configure(int sm_count, int* clusters);
 cudaError_t launch_kv8_tree(const Kv8View& c, const spec_kv8_attention_args& a, const int* clusters, cudaStream_t s);
 
+#ifdef __CUDACC__
+// Heads head0 .. head0 + G - 1 of rows lo .. hi - 1 of out and lse (either may be null): NaN, or those of rows that see
+// nothing.  (Kept out of the kernels: what they seldom run shall not lie among what they always run.)
+static __device__ __noinline__ void kv8_fill(uint16_t* out, int64_t row_stride, float* lse, int n_q_heads, int head0, int G,
+                                             int lo, int hi, bool nan) {
+  const uint32_t w = nan ? 0x7fff7fffu : 0u;  // (NaN in bf16 and in fp16)
+  for (int64_t row = lo + (int)(threadIdx.x >> 4); row < hi; row += blockDim.x >> 4)  // 16 threads each
+    for (int head = head0; head < head0 + G; ++head) {
+      const int at = threadIdx.x & 15;
+      if (out) *reinterpret_cast<uint4*>(out + row_stride * row + (int64_t)head * kKv8Hd + 8 * at) = make_uint4(w, w, w, w);
+      if (lse && at == 0) lse[row * n_q_heads + head] = __int_as_float(nan ? 0x7fffffff : 0xff800000);
+    }
+}
+// What `fill` asks for of rows that no row tile writes, by all threads of one CTA per entry and kv head: the entry's own
+// ones, as NaN, where it is out of range; the rows before the first entry and behind the last one as if they saw nothing.
+__device__ __forceinline__ void kv8_fill_rows(const spec_kv8_attention_args& a, int b, int kvh, int G) {
+  const int first = a.offsets[b], end = a.offsets[b + 1], n = end - first, seq = a.seq_ids ? a.seq_ids[b] : b;
+  const int P = seq >= 0 && seq < a.n_seqs ? a.lengths[seq] : -1;
+  const bool bad = P < 0 || P > a.max_prefix || first < 0 || n < 1 || n > a.max_nodes || n > a.rows - first;
+  if (!bad && b > 0 && b < a.batch - 1) return;
+#pragma unroll 1
+  for (int part = 0; part < 3; ++part) {  // before the first entry, the entry, behind the last
+    const int lo = part == 0 ? 0 : part == 1 ? first : end, hi = part == 0 ? first : part == 1 ? end : a.rows;
+    if (part == 0 ? b == 0 : part == 1 ? bad : b == a.batch - 1)
+      kv8_fill(a.fill & SPEC_KV8_FILL_OUT ? static_cast<uint16_t*>(a.out) : nullptr, a.out_row_stride,
+               a.fill & SPEC_KV8_FILL_LSE ? a.lse : nullptr, a.n_q_heads, kvh * G, G, max(0, lo), min(a.rows, hi), part == 1);
+  }
+}
+#endif
+
 }  // namespace spec

@@ -223,6 +223,7 @@ int spec_kv8_attention(spec_kv8* h, int layer, const spec_kv8_attention_args* a,
   if (!(a->scale >= 0.f) || !std::isfinite(a->scale)) return fail(h, SPEC_ERR_ARG, "scale must be finite and not negative");
   if ((a->k_new == nullptr) != (a->v_new == nullptr)) return fail(h, SPEC_ERR_ARG, "k_new and v_new go together");
   if (a->parents && !a->k_new) return fail(h, SPEC_ERR_ARG, "parents need k_new and v_new");
+  if (a->fill & ~(SPEC_KV8_FILL_OUT | SPEC_KV8_FILL_LSE)) return fail(h, SPEC_ERR_ARG, "unknown bits in fill");
   if (!a->offsets || !a->tables || !a->lengths) return fail(h, SPEC_ERR_ARG, "null pointer");
   if (a->rows == 0) return SPEC_OK;
   if (!a->q || !a->out) return fail(h, SPEC_ERR_ARG, "null pointer");

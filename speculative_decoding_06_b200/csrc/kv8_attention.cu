@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_decode_kernel(const __grid_co
   const int b = bk / c.hkv, kvh = bk - b * c.hkv;
   const int first = a.offsets[b], n = a.offsets[b + 1] - first;
   const int seq = a.seq_ids ? a.seq_ids[b] : b;
+  if (a.fill && row0 == 0 && chunk_i == 0) kv8_fill_rows(a, b, kvh, G);
   if (seq < 0 || seq >= a.n_seqs || first < 0 || n < 1 || n > a.max_nodes || n > a.rows - first) return;
   const int P = a.lengths[seq];
   const int rows = n * G;

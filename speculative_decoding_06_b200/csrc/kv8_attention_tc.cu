@@ -334,6 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
   }
   const int first = a.offsets[b], n = a.offsets[b + 1] - first;
   const int seq = a.seq_ids ? a.seq_ids[b] : b;
+  if (a.fill && row0 == 0 && share == 0) kv8_fill_rows(a, b, kvh, G);
   if (seq < 0 || seq >= a.n_seqs || first < 0 || n < 1 || n > a.max_nodes || n > a.rows - first) return;
   const int P = a.lengths[seq];
   const int rows = n * G;
@@ -691,7 +692,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
       if (lane == 0) mbar_arrive(&bar[B_TREF + tt]);
     }
     for (int tt = 0; tt < nt && ok; ++tt) {
-      const int j = np + tt;
       uint8_t* const op = enter();
       if (!ok) break;
       // V's infinities and NaN become 0, because 0 * NaN would reach rows that do not see them; they are added at
@@ -722,10 +722,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
     const bool warp_on = __any_sync(0xffffffffu, row0 + r < rows);
     // what the row sees of the step's own rows, in the last of the rounds' buffers
     bool ok = true;
-    auto seen = [&](uint64_t& lo, uint64_t& hi) {
+    auto seen = [&](uint64_t& lo, uint64_t& hi) {  // (after B_ANC, or a barrier with warps that waited for it)
       const int node = row0 + r < rows ? by_g(row0 + r) : 0;
       if (a.parents) {
-        if (!held(B_ANC, 0)) ok = false;
         const ulonglong2 set = s_anc[128 * ((32 - __clz(top)) & 1) + node];
         lo = set.x, hi = set.y;
       } else {
@@ -788,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
       uint64_t see = ~0ull;  // keys of the unit that the row sees
       if (u >= np - 1) {
         if (u >= np) {
-          if (ok) ok = held(B_TREF + u - np, 0);
+          if (ok) ok = held(B_TREF + u - np, 0) && (!a.parents || held(B_ANC, 0));
           uint64_t lo, hi;
           seen(lo, hi);
           see = u == np ? lo : hi;

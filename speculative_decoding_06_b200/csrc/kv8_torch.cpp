@@ -228,6 +228,7 @@ PyObject* py_attention(PyObject*, PyObject* const* p, Py_ssize_t n) {
     if (!out) {
       new_out = at::empty({rows, hq, kHd}, q.options());
       out = &new_out;
+      a.fill |= SPEC_KV8_FILL_OUT;  // (nothing of new memory stays as it was)
     } else if (out->scalar_type() != q.scalar_type() || out->dim() != 3 || out->size(0) != rows ||
                (rows && out->stride(1) != kHd)) {
       bad("out must have q's dtype and shape, its heads contiguous");
@@ -238,6 +239,7 @@ PyObject* py_attention(PyObject*, PyObject* const* p, Py_ssize_t n) {
     if (!lse) {
       new_lse = at::empty({rows, hq}, q.options().dtype(at::kFloat));
       lse = &new_lse;
+      a.fill |= SPEC_KV8_FILL_LSE;
     } else if (lse->scalar_type() != at::kFloat || lse->dim() != 2 || lse->size(0) != rows || lse->size(1) != hq ||
                !lse->is_contiguous()) {
       bad("lse must be contiguous fp32 [rows][n_q_heads]");

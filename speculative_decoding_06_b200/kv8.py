@@ -151,8 +151,9 @@ class KV8Cache:
                   workspace: Optional[torch.Tensor] = None):
         """Attention of q's rows ([rows][n_q_heads][128], bf16 or fp16) over the cached prefixes and, with k_new and
         v_new ([rows][n_kv_heads][128]), the step's own rows (spec_kv8_attention).  Entry b holds rows offsets[b] ..
-        offsets[b + 1] - 1, at most max_nodes, of a sequence of at most max_prefix cached tokens.  Returns (out, lse);
-        rows outside every entry are left as they were."""
+        offsets[b + 1] - 1, at most max_nodes, of a sequence of at most max_prefix cached tokens.  Returns (out, lse).
+        Rows outside every entry, and those of an entry that is out of range (its sequence id, length or row count),
+        are left as they were in `out` and `lse`; where these are new, the former are 0 and -inf, the latter NaN."""
         rc, out, lse = _kv8.attention(*self._id, layer, q, tables, lengths, offsets, max_prefix, max_nodes, k_new,
                                       v_new, parents, seq_ids, scale, out, lse, workspace)
         if rc:

@@ -41,6 +41,9 @@ SPEC_KV8_TABLE = 4
 SPEC_KV8_INDEX = 8
 # bytes at the start of an attention workspace that have to be zero before its first use
 SPEC_KV8_WORKSPACE_ZERO = 65536
+# `fill` of spec_kv8_attention
+SPEC_KV8_FILL_OUT = 1
+SPEC_KV8_FILL_LSE = 2
 
 PROF_CLASSES = ("embed_meta", "gemm_qkv", "rope_kv_store", "attention", "gemm_o", "resid_norm", "gemm_gate_up",
                 "gemm_down", "lm_head", "lm_reduce", "accept_walk", "kv_compact", "gemm_layer", "draft_fc", "topk",
@@ -103,7 +106,7 @@ class spec_kv8_attention_args(ctypes.Structure):
                                               "v_row_stride", "v_head_stride", "out_row_stride")] + \
                [(k, ctypes.c_int32) for k in ("dtype", "batch", "n_seqs", "max_blocks", "n_q_heads", "rows",
                                               "max_nodes", "max_prefix")] + \
-               [("scale", ctypes.c_float)]
+               [("scale", ctypes.c_float), ("fill", ctypes.c_int32)]
 
 
 _i32p = ctypes.POINTER(ctypes.c_int32)

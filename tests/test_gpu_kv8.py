@@ -552,3 +552,50 @@ def test_workspace_of_the_largest_bounds_serves_a_draining_batch():
             ws = c["cache"].attention_workspace(40, 8, 20, 900)
             ws[S.SPEC_KV8_WORKSPACE_ZERO:] = 0x7F
         check_attention(c, run_attention(c, workspace=ws), reference(c))
+
+
+@pytest.mark.parametrize("nodes,hq", [([1, 2, 1, 2], 4), ([20, 30, 40, 50], 4), ([2, 2, 3, 1], 12)])
+@pytest.mark.parametrize("given", ["none", "out", "lse"])
+def test_new_outputs_hold_no_old_memory(nodes, hq, given):
+    """Rows before and behind the entries of a new output are those of rows that see nothing, an entry out of range is
+    NaN; buffers that the caller gives keep what they had."""
+    c = attention_case(27, [100, 1500, 80, 70], nodes, hq, 2, 32, "bf16")
+    T, o = sum(nodes), c["offsets"] + 3
+    c["offsets"], c["parents"] = o, np.concatenate([[-1] * 3, c["parents"], [-1] * 4])
+    ref = reference(dict(c, offsets=o - 3, parents=c["parents"][3:-4]))
+    for name in ("q", "k", "v"):
+        c[name] = torch.cat([c[name][:3], c[name], c[name][:4]])
+    c["lengths"][c["ids"][2]] = 1501  # above max_prefix
+    ids = c["ids"].copy()
+    ids[0] = -1
+    old = [torch.full((T + 7, hq, 128), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((T + 7, hq), 7.0, device="cuda")]
+    kw = dict(out=old[0]) if given == "out" else dict(lse=old[1]) if given == "lse" else {}
+    if given != "out":
+        old[0] = None  # (the allocator's next block of this size)
+    if given != "lse":
+        old[1] = None
+    out, lse = run_attention(c, seq_ids=i32(ids), **kw)
+    want_out, want_lse = torch.zeros(T + 7, device="cuda"), torch.full((T + 7,), -math.inf, device="cuda")
+    for b in (0, 2):
+        want_out[o[b]:o[b + 1]] = want_lse[o[b]:o[b + 1]] = math.nan
+    if given == "out":
+        want_out[:] = 7
+    if given == "lse":
+        want_lse[:] = 7
+    for x, want in ((out.float(), want_out[:, None, None]), (lse, want_lse[:, None])):
+        for lo, hi in ((0, o[1]), (o[2], o[3]), (o[4], T + 7)):
+            assert torch.equal(torch.nan_to_num(x[lo:hi], nan=99.0), torch.nan_to_num(want[lo:hi], nan=99.0).expand_as(x[lo:hi]))
+    for b in (1, 3):
+        sl, rs = slice(o[b], o[b + 1]), slice(o[b] - 3, o[b + 1] - 3)
+        check_attention(c, (out[sl], lse[sl]), [x[rs] for x in ref])
+
+
+def test_attention_after_a_plan_that_did_not_fit():
+    """Its offsets are all 0: no entry has rows, and the new outputs say that nothing was seen."""
+    c = attention_case(28, [40, 9], [2, 30], 4, 2, 16, "fp16")
+    out, lse = c["cache"].attention(0, c["q"].cuda(), i32(c["tables"]), i32(c["lengths"]), i32([0, 0, 0]), max_prefix=40,
+                                    max_nodes=30, seq_ids=i32(c["ids"]))
+    assert not out.any() and (lse == -math.inf).all()
+    out, lse = c["cache"].attention(0, c["q"].cuda(), i32(c["tables"]), i32(c["lengths"]), i32([0, 0, 0]), max_prefix=40,
+                                    max_nodes=1, seq_ids=i32(c["ids"]))
+    assert not out.any() and (lse == -math.inf).all()

@@ -240,3 +240,8 @@ def test_workspace_of_random_bounds_serves_all_below_them(handle):
                                              "max_nodes": small[1], "max_prefix": small[2], "out_row_stride": 8192,
                                              "workspace_bytes": workspace(handle, large[0], 64, large[1], large[2])})
             assert S.spec_kv8_attention(handle, 0, ctypes.byref(a), None) == S.SPEC_ERR_CUDA, (large, small, hq)
+
+
+@pytest.mark.parametrize("fill,rc", [(0, S.SPEC_ERR_CUDA), (3, S.SPEC_ERR_CUDA), (4, S.SPEC_ERR_ARG), (-1, S.SPEC_ERR_ARG)])
+def test_attention_fill_bits(handle, fill, rc):
+    assert S.spec_kv8_attention(handle, 0, ctypes.byref(S.spec_kv8_attention_args(**{**ATTN, "fill": fill})), None) == rc
