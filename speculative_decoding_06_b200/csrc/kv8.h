@@ -49,7 +49,7 @@ cudaError_t launch_kv8_tree(const Kv8View& c, const spec_kv8_attention_args& a, 
 static __device__ __noinline__ void kv8_fill(uint16_t* out, int64_t row_stride, float* lse, int n_q_heads, int head0, int G,
                                              int lo, int hi, bool nan) {
   const uint32_t w = nan ? 0x7fff7fffu : 0u;  // (NaN in bf16 and in fp16)
-  for (int64_t row = lo + (int)(threadIdx.x >> 4); row < hi; row += blockDim.x >> 4)  // 16 threads each
+  for (int64_t row = (int64_t)lo + (threadIdx.x >> 4); row < hi; row += blockDim.x >> 4)  // 16 threads each
     for (int head = head0; head < head0 + G; ++head) {
       const int at = threadIdx.x & 15;
       if (out) *reinterpret_cast<uint4*>(out + row_stride * row + (int64_t)head * kKv8Hd + 8 * at) = make_uint4(w, w, w, w);

@@ -348,24 +348,23 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_decode_kernel(const __grid_co
         const __half2 lo = __floats2half2_rn(p0, p1), hi = __floats2half2_rn(p2, p3);
         // (below 2^-14 the rounding loses bits that 2^-w may make matter, and the weight in O is small)
         auto kept = [](float p, float rounded) { return p < 0x1p-14f ? p : rounded; };
-        if (!far) {
-          const float un = fast_exp2(kLift - (u ? ve1 : ve0));
-          l[nt][0] = fmaf(p0 + p2, un, l[nt][0]);
-          l[nt][1] = fmaf(p1 + p3, un, l[nt][1]);
-          lr[nt][0] = fmaf(kept(p0, __low2float(lo)) + kept(p2, __low2float(hi)), un, lr[nt][0]);
-          lr[nt][1] = fmaf(kept(p1, __high2float(lo)) + kept(p3, __high2float(hi)), un, lr[nt][1]);
-        } else {
-          // (rare) the weights themselves, as squares: 2^-149 where one exponential ends at 2^-126
-          const float w = kLift - (u ? ve1 : ve0);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float h = fast_exp2(0.5f * (s[u][nt][q] - (q & 1 ? n1 : n0) + w));
-            l[nt][q & 1] = fmaf(h, h, l[nt][q & 1]);
-            lr[nt][q & 1] = fmaf(h, h, lr[nt][q & 1]);
-          }
-        }
+        const float un = far ? 0.f : fast_exp2(kLift - (u ? ve1 : ve0));
+        l[nt][0] = fmaf(p0 + p2, un, l[nt][0]);
+        l[nt][1] = fmaf(p1 + p3, un, l[nt][1]);
+        lr[nt][0] = fmaf(kept(p0, __low2float(lo)) + kept(p2, __low2float(hi)), un, lr[nt][0]);
+        lr[nt][1] = fmaf(kept(p1, __high2float(lo)) + kept(p3, __high2float(hi)), un, lr[nt][1]);
         pb[u][nt][0] = transpose8x8(*reinterpret_cast<const uint32_t*>(&lo));
         pb[u][nt][1] = transpose8x8(*reinterpret_cast<const uint32_t*>(&hi));
+      }
+    }
+    if (far) {  // (rare) the weights themselves, as squares: 2^-149 where one exponential ends at 2^-126
+#pragma unroll
+      for (int i2 = 0; i2 < 8 * NT; ++i2) {
+        const int u = i2 & 1, q = i2 >> 1 & 3, nt = i2 >> 3, col = q & 1;
+        const float n = m[nt][col] == -INFINITY ? 0.f : m[nt][col];
+        const float h = fast_exp2(0.5f * (s[u][nt][q] - n + kLift - (u ? ve1 : ve0)));
+        l[nt][col] = fmaf(h, h, l[nt][col]);
+        lr[nt][col] = fmaf(h, h, lr[nt][col]);
       }
     }
 #pragma unroll
