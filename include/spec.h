@@ -474,7 +474,7 @@ typedef struct spec_kv8_plan_args {
   int32_t batch;           /* 1 .. 8192 */
   int32_t n_seqs;          /* 1 .. 65536 */
   int32_t max_blocks;
-  int32_t max_rows;        /* >= 0 */
+  int32_t max_rows;        /* 0 .. 2^30 */
 } spec_kv8_plan_args;
 SPEC_API int spec_kv8_plan(spec_kv8* h, const spec_kv8_plan_args* a, void* cuda_stream);
 
@@ -495,7 +495,7 @@ typedef struct spec_kv8_append_args {
   const int32_t* src_rows; /* [rows], or NULL */
   int64_t k_row_stride, k_head_stride, v_row_stride, v_head_stride; /* in elements; rows of 16-byte alignment */
   int32_t dtype;           /* SPEC_DTYPE_F32, _BF16 or _F16 */
-  int32_t rows;
+  int32_t rows;            /* 0 .. 2^30 */
   int32_t n_src;
 } spec_kv8_append_args;
 SPEC_API int spec_kv8_append(spec_kv8* h, int layer, const spec_kv8_append_args* a, void* cuda_stream);

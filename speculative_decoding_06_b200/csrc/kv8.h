@@ -18,6 +18,8 @@ constexpr int kKv8MaxBatch = 8192;
 constexpr int kKv8MaxSeqs = 65536;
 constexpr int kKv8MaxGroup = 64;  // query heads per kv head
 constexpr int kKv8MaxNodes = 128;
+constexpr int kKv8MaxRows = 1 << 30;    // of an append, of a plan: numbered in 32 bits, a grid's stride beyond the last one
+constexpr int kKv8MaxGroups = 1 << 30;  // row tiles of an attention call of few rows, numbered likewise
 constexpr int kKv8TcMaxChunks = 8;     // CTAs of a cluster that share a sequence's prefix (tree kernel)
 constexpr int kKv8TcMaxKeys = 49152;   // keys of one of them
 
@@ -33,7 +35,8 @@ cudaError_t kv8_plan_configure();
 cudaError_t launch_kv8_plan(const spec_kv8_plan_args& a, int page_log2, int n_pages, cudaStream_t s);
 cudaError_t launch_kv8_append(const Kv8View& c, const spec_kv8_append_args& a, int sm_count, cudaStream_t s);
 cudaError_t kv8_attention_configure(int sm_count, int* clusters);
-// workspace bytes that a call of these bounds needs; that every call up to these bounds needs
+// workspace bytes that a call of these bounds needs (0: more than kKv8MaxGroups row tiles); that every call up to these
+// bounds needs
 size_t kv8_attention_need(const Kv8View& c, int sm_count, int batch, int n_q_heads, int max_nodes, int max_prefix);
 size_t kv8_attention_workspace(const Kv8View& c, int sm_count, int batch, int n_q_heads, int max_nodes, int max_prefix);
 cudaError_t launch_kv8_attention(const Kv8View& c, const CUtensorMap& map, const spec_kv8_attention_args& a, const int* clusters, cudaStream_t s);

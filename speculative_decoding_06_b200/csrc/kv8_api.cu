@@ -166,6 +166,7 @@ int spec_kv8_plan(spec_kv8* h, const spec_kv8_plan_args* a, void* cuda_stream) {
     return fail(h, SPEC_ERR_ARG, "batch %d above n_seqs %d without seq_ids", a->batch, a->n_seqs);
   if (a->batch > kKv8MaxBatch || a->n_seqs > kKv8MaxSeqs)
     return fail(h, SPEC_ERR_CAPACITY, "batch above %d or n_seqs above %d", kKv8MaxBatch, kKv8MaxSeqs);
+  if (a->max_rows > kKv8MaxRows) return fail(h, SPEC_ERR_CAPACITY, "max_rows above %d", kKv8MaxRows);
   if ((int64_t)a->max_blocks * h->cfg.page >= ((int64_t)1 << 31))
     return fail(h, SPEC_ERR_CAPACITY, "max_blocks * page has to be below 2^31");
   if (int rc = check_device(h)) return rc;
@@ -182,6 +183,7 @@ int spec_kv8_append(spec_kv8* h, int layer, const spec_kv8_append_args* a, void*
     return fail(h, SPEC_ERR_ARG, "%d rows from %d source rows without src_rows", a->rows, a->n_src);
   if (a->dtype != SPEC_DTYPE_F32 && a->dtype != SPEC_DTYPE_BF16 && a->dtype != SPEC_DTYPE_F16)
     return fail(h, SPEC_ERR_ARG, "dtype must be SPEC_DTYPE_F32, SPEC_DTYPE_BF16 or SPEC_DTYPE_F16");
+  if (a->rows > kKv8MaxRows) return fail(h, SPEC_ERR_CAPACITY, "more than %d rows", kKv8MaxRows);
   if (a->rows == 0) return SPEC_OK;
   if (!a->k || !a->v || !a->slots) return fail(h, SPEC_ERR_ARG, "null pointer");
   const int es = a->dtype == SPEC_DTYPE_F32 ? 4 : 2;
@@ -195,7 +197,8 @@ int spec_kv8_append(spec_kv8* h, int layer, const spec_kv8_append_args* a, void*
 
 size_t spec_kv8_attention_workspace(spec_kv8* h, int batch, int n_q_heads, int max_nodes, int max_prefix) {
   if (!h || batch < 1 || n_q_heads < 1 || n_q_heads % h->cfg.n_kv_heads ||
-      n_q_heads / h->cfg.n_kv_heads > kKv8MaxGroup || max_nodes < 1 || max_nodes > kKv8MaxNodes || max_prefix < 0)
+      n_q_heads / h->cfg.n_kv_heads > kKv8MaxGroup || max_nodes < 1 || max_nodes > kKv8MaxNodes || max_prefix < 0 ||
+      kv8_attention_need(view_of(h, 0), h->sm_count, batch, n_q_heads, max_nodes, max_prefix) == 0)
     return 0;
   return kv8_attention_workspace(view_of(h, 0), h->sm_count, batch, n_q_heads, max_nodes, max_prefix);
 }
@@ -234,8 +237,9 @@ int spec_kv8_attention(spec_kv8* h, int layer, const spec_kv8_attention_args* a,
     return fail(h, SPEC_ERR_ARG, "q, k_new, v_new and out rows must be 16-byte aligned, with strides of whole 16-byte units");
   if (a->out_row_stride < (int64_t)a->n_q_heads * kKv8Hd) return fail(h, SPEC_ERR_ARG, "out rows overlap");
   if (!a->workspace || !aligned16(a->workspace)) return fail(h, SPEC_ERR_ARG, "workspace is null or not 16-byte aligned");
-  if (a->workspace_bytes <
-      kv8_attention_need(view_of(h, 0), h->sm_count, a->batch, a->n_q_heads, a->max_nodes, a->max_prefix))
+  const size_t need = kv8_attention_need(view_of(h, 0), h->sm_count, a->batch, a->n_q_heads, a->max_nodes, a->max_prefix);
+  if (need == 0) return fail(h, SPEC_ERR_CAPACITY, "more than %d row tiles (batch * n_kv_heads and more)", kKv8MaxGroups);
+  if (a->workspace_bytes < need)
     return fail(h, SPEC_ERR_CAPACITY, "workspace too small");
   if (int rc = check_device(h)) return rc;
   spec_kv8_attention_args b = *a;

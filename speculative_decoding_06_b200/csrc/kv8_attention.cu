@@ -578,6 +578,7 @@ bool by_tree(int hkv, int n_q_heads, int max_nodes, int max_prefix) {
 
 size_t kv8_attention_need(const Kv8View& c, int sm_count, int batch, int n_q_heads, int max_nodes, int max_prefix) {
   if (by_tree(c.hkv, n_q_heads, max_nodes, max_prefix)) return 16;
+  if ((long long)batch * c.hkv * ((max_nodes * (n_q_heads / c.hkv) + 15) / 16) > kKv8MaxGroups) return 0;
   int nt = 1;
   size_t bytes = 0;
   plan_decode(c.hkv, sm_count, batch, n_q_heads, max_nodes, max_prefix, &nt, &bytes);

@@ -245,3 +245,31 @@ def test_workspace_of_random_bounds_serves_all_below_them(handle):
 @pytest.mark.parametrize("fill,rc", [(0, S.SPEC_ERR_CUDA), (3, S.SPEC_ERR_CUDA), (4, S.SPEC_ERR_ARG), (-1, S.SPEC_ERR_ARG)])
 def test_attention_fill_bits(handle, fill, rc):
     assert S.spec_kv8_attention(handle, 0, ctypes.byref(S.spec_kv8_attention_args(**{**ATTN, "fill": fill})), None) == rc
+
+
+# ---------------------------------------------------------------- counts near 2^31
+@pytest.mark.parametrize("rows,rc", [(1 << 30, S.SPEC_ERR_CUDA), ((1 << 30) + 1, S.SPEC_ERR_CAPACITY),
+                                     ((1 << 31) - 100, S.SPEC_ERR_CAPACITY)])
+def test_rows_that_32_bits_do_not_number(handle, rows, rc):
+    """The kernels number rows in 32 bits, up to a grid's stride behind the last one."""
+    a = S.spec_kv8_append_args(**{**APPEND, "rows": rows, "n_src": 9})
+    assert S.spec_kv8_append(handle, 0, ctypes.byref(a), None) == rc
+    a = S.spec_kv8_plan_args(**{**PLAN, "max_rows": rows})
+    assert S.spec_kv8_plan(handle, ctypes.byref(a), None) == rc
+
+
+def test_more_groups_than_32_bits_number():
+    """65535 entries times 65535 kv heads: refused, where the number of row groups wrapped around and nothing was done."""
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are made up")
+    c, h = config(n_layers=1, n_kv_heads=65535, page=16, n_pages=1), ctypes.c_void_p()
+    assert S.spec_kv8_open(ctypes.byref(c), 1 << 20, 1 << 40, 1 << 21, 1 << 40, ctypes.byref(h)) == S.SPEC_OK
+    try:
+        for batch, nodes, rc in ((16384, 1, S.SPEC_ERR_CUDA), (16385, 1, S.SPEC_ERR_CAPACITY), (65535, 1, S.SPEC_ERR_CAPACITY),
+                                 (65535, 17, S.SPEC_ERR_CUDA)):  # (17 rows: the kernel of another grid)
+            a = S.spec_kv8_attention_args(**{**ATTN, "n_q_heads": 65535, "out_row_stride": 65535 * 128, "batch": batch,
+                                             "n_seqs": batch, "max_nodes": nodes, "max_blocks": 64, "max_prefix": 1000})
+            assert S.spec_kv8_attention(h, 0, ctypes.byref(a), None) == rc
+            assert (workspace(h, batch, 65535, nodes, 1000) == 0) == (rc == S.SPEC_ERR_CAPACITY)
+    finally:
+        S.spec_kv8_close(h)
