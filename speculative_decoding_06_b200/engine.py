@@ -351,7 +351,9 @@ class SpecEngine:
         """Store the cached K/V of sequences into an 8-bit paged cache (kv8.KV8Cache with the target's layers and kv
         heads; a third of the dense cache's bytes), so that their places here can be reused while the prefixes stay
         readable by KV8Cache.attention.  pages: cache.page_state(...), updated in place; engine sequence seq_ids[i]
-        extends sequence kv8_ids[i] (default: i) there.  bf16 models only.  Returns the token counts."""
+        extends sequence kv8_ids[i] (default: i) there.  bf16 models only; of K, whose low bits lie in a plane of their
+        own, the fp16 part is stored.  Waits for the plan (whether the tokens fit); the rows are then queued on the
+        current stream of the cache's device.  Returns the token counts."""
         d = self.dims
         if d.dtype != "bf16":
             raise ValueError("export_kv8 needs a bf16 model (its cache is fp16)")
@@ -359,6 +361,8 @@ class SpecEngine:
         if (cache.n_layers, cache.n_kv_heads) != (d.n_layers, d.n_kv_heads):
             raise ValueError("the 8-bit cache has %d layers of %d kv heads, the target model %d of %d" % (
                 cache.n_layers, cache.n_kv_heads, d.n_layers, d.n_kv_heads))
+        if kv.device != cache.device:
+            raise ValueError("the engine is on %s, the 8-bit cache on %s" % (kv.device, cache.device))
         ids = [int(s) for s in seq_ids]
         to = list(range(len(ids))) if kv8_ids is None else [int(s) for s in kv8_ids]
         lens = [self.seq_len(s)[0] for s in ids]
@@ -374,12 +378,14 @@ class SpecEngine:
         max_seq, heads = kv.shape[4], d.n_kv_heads
         src = torch.cat([torch.arange(n, **i32) + s * heads * max_seq for s, n in zip(ids, lens)])
         n_src = (kv.shape[2] * heads - (heads - 1)) * max_seq
-        torch.cuda.current_stream().wait_stream(self.stream)
+        current = torch.cuda.current_stream(dev)
+        current.wait_stream(self.stream)
         for layer in range(d.n_layers):
             k, v = (kv.as_strided((n_src, heads, d.head_dim), (d.head_dim, max_seq * d.head_dim, 1),
                                   kv[layer, plane].storage_offset()) for plane in (0, 1))
             cache.append(layer, k, v, plan.slots, src_rows=src)
-        self.stream.wait_stream(torch.cuda.current_stream())
+        self.kv.record_stream(current)  # (an engine may be closed while its rows are still being stored)
+        self.stream.wait_stream(current)
         return lens
 
     def kv_view(self) -> torch.Tensor:
