@@ -64,14 +64,14 @@ int32_t* ints(const at::Tensor* t, const Cache& c, const char* name, int64_t d0,
   return t->data_ptr<int32_t>();
 }
 
-// [rows][heads][128] with contiguous values of a head
+// [rows][heads][128] with contiguous values of a head (the stride of a dimension of one counts for nothing)
 void rows_of(const at::Tensor& t, const Cache& c, const char* name, int64_t heads, int64_t* row_stride,
              int64_t* head_stride) {
   on_device(t, c, name);
   if (t.dim() != 3 || t.size(1) != heads || t.size(2) != kHd || (t.numel() && t.stride(2) != 1))
     bad("%s must be [rows][%lld][128] with contiguous values", name, (long long)heads);
-  *row_stride = t.stride(0);
-  *head_stride = t.stride(1);
+  *head_stride = heads == 1 ? kHd : t.stride(1);
+  *row_stride = t.size(0) <= 1 ? heads * kHd : t.stride(0);
 }
 
 int dtype_of(const at::Tensor& t, const char* name) {
@@ -230,7 +230,7 @@ PyObject* py_attention(PyObject*, PyObject* const* p, Py_ssize_t n) {
       out = &new_out;
       a.fill |= SPEC_KV8_FILL_OUT;  // (nothing of new memory stays as it was)
     } else if (out->scalar_type() != q.scalar_type() || out->dim() != 3 || out->size(0) != rows ||
-               (rows && out->stride(1) != kHd)) {
+               (rows && hq > 1 && out->stride(1) != kHd)) {
       bad("out must have q's dtype and shape, its heads contiguous");
     }
     int64_t head_stride;

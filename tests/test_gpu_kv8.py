@@ -599,3 +599,23 @@ def test_attention_after_a_plan_that_did_not_fit():
     out, lse = c["cache"].attention(0, c["q"].cuda(), i32(c["tables"]), i32(c["lengths"]), i32([0, 0, 0]), max_prefix=40,
                                     max_nodes=1, seq_ids=i32(c["ids"]))
     assert not out.any() and (lse == -math.inf).all()
+
+
+@pytest.mark.parametrize("nodes,hkv", [(1, 1), (3, 1), (1, 2)])
+def test_strides_of_dimensions_of_one_do_not_matter(nodes, hkv):
+    """One head, or one row: what stride that dimension has is never used."""
+    c = attention_case(29, [70], [nodes], hkv, hkv, 32, "bf16")
+    if hkv == 1:
+        odd = lambda t: t.cuda().as_strided((nodes, 1, 128), (128, 3, 1))  # noqa: E731
+        out = torch.empty(1, nodes, 128, dtype=torch.bfloat16, device="cuda").transpose(0, 1)
+    else:
+        odd = lambda t: t.cuda().as_strided((1, hkv, 128), (5, 128, 1))  # noqa: E731
+        out = torch.empty(hkv, 1, 128, dtype=torch.bfloat16, device="cuda").transpose(0, 1)
+    got = run_attention(c, q=odd(c["q"]), k_new=odd(c["k"]), v_new=odd(c["v"]), out=out)
+    assert got[0].data_ptr() == out.data_ptr()
+    check_attention(c, got, reference(c))
+    one = make_cache(4, hkv, 32, garbage=0)
+    two = make_cache(4, hkv, 32, garbage=0)
+    one.append(0, c["k"].cuda(), c["v"].cuda(), i32(np.arange(nodes) + 64))
+    two.append(0, odd(c["k"]), odd(c["v"]), i32(np.arange(nodes) + 64))
+    assert torch.equal(one.codes, two.codes) and torch.equal(one.exps, two.exps)
