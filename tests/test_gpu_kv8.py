@@ -619,3 +619,50 @@ def test_strides_of_dimensions_of_one_do_not_matter(nodes, hkv):
     one.append(0, c["k"].cuda(), c["v"].cuda(), i32(np.arange(nodes) + 64))
     two.append(0, odd(c["k"]), odd(c["v"]), i32(np.arange(nodes) + 64))
     assert torch.equal(one.codes, two.codes) and torch.equal(one.exps, two.exps)
+
+
+def plain64(cache, table, P, q, k, v):
+    """Attention of a chain's rows over one kv head's prefix in 64 bits on the GPU: (out, lse, mass, score size)."""
+    pages = table[:-(-P // cache.page)].long()
+    kv = []
+    for plane in (0, 1):
+        x = cache.codes[0, plane, pages, 0].view(torch.float8_e4m3fn).double()
+        x *= torch.exp2(cache.exps[0, plane, pages, 0].double() - 127)[:, None, None]
+        kv.append(torch.cat([x.reshape(-1, 128)[:P], (k, v)[plane][:, 0].double()]))
+    n, hq = q.shape[:2]
+    s = torch.einsum("nhd,kd->nhk", q.double(), kv[0]) * 128 ** -0.5
+    see = torch.arange(P + n, device="cuda")[None, :] <= P + torch.arange(n, device="cuda")[:, None]
+    s.masked_fill_(~see[:, None, :], -math.inf)
+    p = torch.softmax(s, 2)
+    size = torch.einsum("nhd,kd->nhk", q.double().abs(), kv[0].abs()).amax(2) * 128 ** -0.5
+    return [x.cpu().numpy() for x in (p @ kv[1], torch.logsumexp(s, 2), p @ kv[1].abs(), size)]
+
+
+@pytest.mark.parametrize("P,bound,copies,n,hq,page", [
+    (49100, 49152, 160, 9, 2, 64),     # a CTA per tile, as many units as a CTA takes
+    (100, 100000, 1, 30, 4, 16), (100000, 100000, 2, 5, 4, 128),  # bounds that need a cluster
+    (393206, 393216, 1, 9, 2, 64),     # shares as long as they can be
+    (65, 393216, 3, 20, 1, 32), (70000, 393216, 1, 17, 1, 16)])
+def test_long_prefixes_of_trees(P, bound, copies, n, hq, page):
+    g = torch.Generator(device="cuda").manual_seed(P)
+    blocks = -(-bound // page)
+    used = -(-P // page)
+    cache = make_cache(used + 3, 1, page, garbage=0x7F)
+    table = torch.randperm(used + 3, generator=g, device="cuda")[:used].to(torch.int32)
+    x = torch.randint(0, 118, (1, 2, used + 3, 1, page, 128), generator=g, device="cuda", dtype=torch.uint8)
+    x += 128 * torch.randint(0, 2, x.shape, generator=g, device="cuda", dtype=torch.uint8)
+    if P % page:
+        x[0, :, table[-1].long(), :, P % page:] = 0x7F
+    cache.codes.copy_(x)
+    cache.exps.copy_(120 + torch.randint(-2, 3, cache.exps.shape, generator=g, device="cuda"))
+    tables = torch.full((1, blocks), -1, dtype=torch.int32, device="cuda")
+    tables[0, :used] = table
+    q, k, v = (torch.randn(n, h, 128, device="cuda", generator=g).half() for h in (hq, 1, 1))
+    many = lambda t: t.repeat(copies, 1, 1)  # noqa: E731
+    out, lse = cache.attention(0, many(q), tables, i32([P]), i32(np.arange(copies + 1) * n), max_prefix=bound, max_nodes=n,
+                               k_new=many(k), v_new=many(v), seq_ids=i32([0] * copies))
+    ref = plain64(cache, table, P, q, k, v)
+    # beyond the bound for 2^14 keys: sums in 32 bits, one after the other, of four products for each unit of 64 keys
+    ref[3] = ref[3] + 4 * (P / 64) * 2.0 ** -23 / (2 * 130 * 2.0 ** -24)
+    check_attention(dict(dtype="fp16"), (out[:n], lse[:n]), ref)
+    assert torch.equal(out, many(out[:n])) and torch.equal(lse, lse[:n].repeat(copies, 1))
