@@ -49,7 +49,7 @@ cudaError_t launch_kv8_tree(const Kv8View& c, const spec_kv8_attention_args& a, 
 #ifdef __CUDACC__
 // Heads head0 .. head0 + G - 1 of rows lo .. hi - 1 of out and lse (either may be null): NaN, or those of rows that see
 // nothing.  (Kept out of the kernels: what they seldom run shall not lie among what they always run.)
-static __device__ __noinline__ void kv8_fill(uint16_t* out, int64_t row_stride, float* lse, int n_q_heads, int head0, int G,
+inline __device__ __noinline__ void kv8_fill(uint16_t* out, int64_t row_stride, float* lse, int n_q_heads, int head0, int G,
                                              int lo, int hi, bool nan) {
   const uint32_t w = nan ? 0x7fff7fffu : 0u;  // (NaN in bf16 and in fp16)
   for (int64_t row = (int64_t)lo + (threadIdx.x >> 4); row < hi; row += blockDim.x >> 4)  // 16 threads each

@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_decode_kernel(const __grid_co
       for (int i = 0; i < 32; ++i) m = fmaxf(m, finite_abs(v[i]));
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      ex = max(-100, min(100, (__float_as_int(m) >> 23) - 127 - 8));
+      ex = max(-120, min(120, (__float_as_int(m) >> 23) - 127 - 8));
     }
     const float f = __int_as_float((127 - ex) << 23);
 #pragma unroll
@@ -417,12 +417,13 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_decode_kernel(const __grid_co
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&qf[nt][i]));
-          x = fmaf(q.x, k[2 * i], x);
-          x = fmaf(q.y, k[2 * i + 1], x);
+          // (q goes up to 2^9, k to the end of the floats)
+          x = fmaf(q.x, 0x1p-16f * k[2 * i], x);
+          x = fmaf(q.y, 0x1p-16f * k[2 * i + 1], x);
         }
         x += __shfl_xor_sync(0xffffffffu, x, 1);
         x += __shfl_xor_sync(0xffffffffu, x, 2);
-        x *= qs[nt];
+        x *= 0x1p16f * qs[nt];
         const bool sees = (s_anc[2 * (8 * nt + g) + (j >> 6)] >> (j & 63)) & 1;
         x = sees ? x : -INFINITY;
 #pragma unroll

@@ -171,7 +171,7 @@ __device__ __forceinline__ uint32_t mul_h2(uint32_t v, __half2 f) {
   return *reinterpret_cast<const uint32_t*>(&y);
 }
 // the exponent that brings values up to `amax` below 2^7 (0 where all are 0)
-__device__ __forceinline__ int shift_of(float amax, int least = -100) {
+__device__ __forceinline__ int shift_of(float amax, int least = -120) {
   const int e = (__float_as_int(amax) >> 23) - 127 - 6;
   return amax > 0.f ? max(least, min(120, e)) : 0;
 }
@@ -672,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const uint16_t bits = (uint16_t)max(red[lane + 32 * k], red[64 + lane + 32 * k]);
-        e[k] = shift_of(to_f32<T>(*reinterpret_cast<const T*>(&bits)), p ? -80 : -100);
+        e[k] = shift_of(to_f32<T>(*reinterpret_cast<const T*>(&bits)), p ? -80 : -120);
         zero[k] = bits == 0;
         most = zero[k] ? most : max(most, e[k]);
         least = zero[k] ? least : min(least, e[k]);

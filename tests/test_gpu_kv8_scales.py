@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import kv8 as O
 from test_gpu_kv8 import attention_case, check_attention, i32, reference, run_attention
 
 pytestmark = pytest.mark.gpu
@@ -128,7 +129,6 @@ def test_large_rows_reach_only_the_rows_that_see_them(prefixes, nodes, hq, size,
     out, lse = run_attention(c)
     rows = torch.from_numpy(fine).cuda()
     check_attention(c, (out[rows], lse[rows]), [x[fine] for x in ref])
-    assert not torch.isnan(out).any() and not torch.isnan(lse).any()
 
 
 @pytest.mark.parametrize("nodes", [[3], [61], [128]])
@@ -150,3 +150,39 @@ def test_scores_that_vanish(prefixes, nodes, tree):
     set_exps(c, 0, lambda b, j: 67)
     check_attention(c, run_attention(c), reference(c))
     check_attention(c, run_attention(c, scale=1e-38), reference(c, 1e-38))
+
+
+@pytest.mark.parametrize("nodes", [1, 3, 40])
+def test_small_rows_of_q_over_keys_near_the_largest_float(nodes):
+    """Scores of ordinary size whose factors are far from it, in the step's own rows and in the prefix."""
+    c = attention_case(37, [40], [nodes], 4, 1, 16, "bf16", "chain")
+    c["k"] = (c["k"].float() * 2.0 ** 120).to(torch.bfloat16)
+    set_exps(c, 0, lambda b, j: 127 + 112)
+    c["q"] = (c["q"].float() * 2.0 ** -120).to(torch.bfloat16)
+    check_attention(c, run_attention(c), reference(c))
+
+
+@pytest.mark.parametrize("nodes", [1, 3, 40])
+def test_the_largest_scores(nodes):
+    """Scores up to 2^21, where those in 32 bits lie 2^-3 apart (in powers of two): the best key has the weight."""
+    c = attention_case(38, [40], [nodes], 4, 1, 16, "bf16", "chain")
+    ref = reference(c)
+    gain = 2.0 ** np.floor(np.log2(2.0 ** 21 / ref[3].max()))
+    c["q"] = (c["q"].float() * gain).to(torch.bfloat16)
+    got, (out, lse, mass, size) = run_attention(c), reference(c)
+    assert size.max() > 2.0 ** 20
+    # a score is off by at most 2^-13 of its own size: keys further below the best one weigh nothing
+    d = 2 * 130 * 2.0 ** -24 * size
+    assert (np.abs(got[1].double().cpu().numpy() - lse) <= d + 1).all()
+    sure = np.zeros(lse.shape, bool)
+    for i in range(nodes):
+        for h in range(4):
+            codes = O.E4M3[c["codes"][0][c["tables"][c["ids"][0], :3], 0].reshape(-1, 128)[:40]]
+            e = np.repeat(c["exps"][0][c["tables"][c["ids"][0], :3], 0].astype(float) - 127, 16)[:40]
+            keys = np.concatenate([codes * 2.0 ** e[:, None], c["k"][:i + 1, 0].double().numpy()])
+            s = np.sort(128 ** -0.5 * keys @ c["q"][i, h].double().numpy())
+            sure[i, h] = s[-1] - s[-2] > 2 * d[i, h] + 30
+    assert sure.any()
+    o = got[0].double().cpu().numpy()
+    assert (np.abs(o - out)[sure] <= 2.0 ** -8 * np.abs(out)[sure] + 2.0 ** -11 * mass[sure] + 1e-7).all()
+    assert np.isfinite(o).all()
