@@ -47,6 +47,13 @@ cudaError_t kv8_tree_configure(int sm_count, int* clusters);
 cudaError_t launch_kv8_tree(const Kv8View& c, const spec_kv8_attention_args& a, const int* clusters, cudaStream_t s);
 
 #ifdef __CUDACC__
+// m + log2 l for a normal l > 0: l's exponent is added to m, which is of its size and the other sign, so that what rounds
+// is of the result's size
+__device__ __forceinline__ float kv8_log2_sum(float m, float l) {
+  const int bits = __float_as_int(l);
+  const float mantissa = __int_as_float((bits & 0x7fffff) | 0x3f800000);
+  return l < INFINITY ? (m + (float)((bits >> 23) - 127)) + log2f(mantissa) : m + l;
+}
 // Heads head0 .. head0 + G - 1 of rows lo .. hi - 1 of out and lse (either may be null): NaN, or those of rows that see
 // nothing.  (Kept out of the kernels: what they seldom run shall not lie among what they always run.)
 inline __device__ __noinline__ void kv8_fill(uint16_t* out, int64_t row_stride, float* lse, int n_q_heads, int head0, int G,

@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_decode_kernel(const __grid_co
     *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(w);
     if (a.lse && lane == 0)
       a.lse[(size_t)(first + node) * a.n_q_heads + head] =
-          ll == 0.f ? -INFINITY : (mm - kLift + log2f(ll)) * 0.69314718055994531f;
+          ll == 0.f ? -INFINITY : kv8_log2_sum(mm - kLift, ll) * 0.69314718055994531f;
   };
   const size_t slot = (size_t)group * pl.chunks + chunk_i;
   for (int r = warp; r < kRows && row0 + r < rows; r += kWarps) {

@@ -916,7 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tree_kernel(Kv8View c, spec_k
     // staged over operands that are done with (B_O follows every MMA) where a cluster shares the prefix.
     // (2^kLift, and a quarter until the end: 448 * 2^120 is more than a float holds, a share of it may not be)
     float inv = !ok ? NAN : l == 0.f ? 0.f : 1024.f / lr;
-    float lse = !ok ? NAN : l == 0.f ? -INFINITY : m - kLift + log2f(l);
+    float lse = !ok ? NAN : l == 0.f ? -INFINITY : kv8_log2_sum(m - kLift, l);
     const bool o_on = ok && n_own > 0;  // (uniform: else O was never written)
     if (o_on) tc_fence_after();
     const uint32_t sw = (uint32_t)(r & 7) << 4;

@@ -186,3 +186,13 @@ def test_the_largest_scores(nodes):
     o = got[0].double().cpu().numpy()
     assert (np.abs(o - out)[sure] <= 2.0 ** -8 * np.abs(out)[sure] + 2.0 ** -11 * mass[sure] + 1e-7).all()
     assert np.isfinite(o).all()
+
+
+@pytest.mark.parametrize("nodes,hq", [([1] * 60, 64), ([40] * 3, 64)])
+@pytest.mark.parametrize("k,v", [(106, 73), (108, 76), (106, 80), (119, 67), (108, 100), (108, 150)])
+def test_log_sum_exp_of_small_scores(nodes, hq, k, v):
+    """Scores near 0 over few keys, whatever V's scale: the log-sum-exp is right to a few steps of its own size."""
+    c = attention_case(39, [2 + i % 9 for i in range(len(nodes))], nodes, hq, 1, 16, "bf16", "none")
+    set_exps(c, 0, lambda b, j: k)
+    set_exps(c, 1, lambda b, j: v)
+    check_attention(c, run_attention(c), reference(c))
