@@ -11,13 +11,16 @@
 // page's exponent byte 255, which reads as NaN and stays until the page is opened
 // anew (place 0): the codes themselves need no NaN, and their readers no test.
 //
-// Prompts read and write each byte once: 195 MB of bf16 rows and their codes take 40 us, 4.9 TB/s, three quarters of the
-// measured copy rate.  A page's rows wait in registers for its largest value, so that the reads in flight are what four
+// Prompts in pages of up to 64 tokens read and write each byte once: 195 MB of bf16 rows and their codes take 40 us,
+// 4.9 TB/s, three quarters of the measured copy rate.  A page's rows wait in registers for its largest value, so that the reads in flight are what four
 // CTAs of 256 threads per SM hold (three: 63 us before the instructions were cut; shared memory in place of registers,
 // six CTAs: 43 where registers took 42); issue slots are busy two thirds of the time, for the magnitudes, the products
-// and the conversions.  Tried without gain: heads of a row side by side in the grid, prefetch into L2 while the slots
+// and the conversions.  Runs of more rows than the registers hold are read a second time, mostly from L2: 64 rows here, so
+// all of a page of 128 (31.7k whole pages of bf16: 41.8 us, 36.6 in pages of 64; fp32 67.0 and 59.7), 16 rows in the CTAs
+// of decoding steps.  Pages of 16 make CTAs of 16 rows, whose loads do not fill an SM (88.5 us, fp32 150).  Tried without gain: heads of a row side by side in the grid, prefetch into L2 while the slots
 // are read, loads that bypass L1, CTAs of 512 threads (51 us).  Steps of a few rows are bound by the chain of loads:
-// slots, rows and the page's exponent, codes before the run where it grows (64 rows: 3.3 us; 317 gathered rows of 64 sequences in fp32: 6.1 us).
+// slots, rows and the page's exponent (64 rows: 3.4 us; 317 gathered rows of 64 sequences in fp32: 6.3 us); where a page's
+// scale grows, the codes before the run too (64 rows, all of whose pages grow: 8.0 us, 3.1 where none does).
 #include <cuda_fp8.h>
 
 #include "common.cuh"

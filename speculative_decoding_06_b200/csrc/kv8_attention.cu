@@ -27,10 +27,13 @@
 // Each warp streams tiles of 32 keys through a queue of its own in shared memory,
 // two tiles deep, which one lane fills by TMA (boxes of 16 keys, each inside one
 // page; the 128-byte swizzle keeps both products' reads free of bank conflicts).
-// A batch of 64 at 512 - 4096 tokens (310 MB) takes 60.5 us, 5.1 TB/s, 78 % of the
-// measured copy rate, with three CTAs of four warps per SM; 68 us with three tiles
+// A batch of 64 at 512 - 4096 tokens (310 MB) takes 61.4 us, 5.0 TB/s, 77 % of the
+// measured copy rate, with three CTAs of four warps per SM (60.1 before l was made to hold for
+// pages of any scale).  Measured beside each other, 60.5 us: 68 us with three tiles
 // and two CTAs, 70 - 110 us with CTAs of two or eight warps, 89 us with sixteen
-// cp.async per lane and tile in place of TMA.  The step's own rows (16-bit K and V) are added by
+// cp.async per lane and tile in place of TMA.  Tiles of 16 rows keep some 200 bytes per thread in local memory
+// (168 registers for three CTAs per SM): 64 sequences of 2400 tokens with 4 rows of 32 query heads on 8 take
+// 94 us, 3.3 TB/s, where 2 rows, tiles of 8, take 68.  The step's own rows (16-bit K and V) are added by
 // plain 32-bit arithmetic.  Warps, then the CTAs of a sequence cut into chunks,
 // merge their (m, l, O); of the latter the one that arrives last, in chunk order,
 // so that results do not depend on the order of arrival.

@@ -23,7 +23,8 @@
 // 512, the exponentials 512 of the special-function units, shared memory 770 (codes in and out, operands in and out)
 // and the instructions of softmax and conversion some 700 of the issue slots; the rest is the latency of a unit's
 // chain (codes to operand, tensor memory to registers and back, six barriers).  Start and end of a CTA take 9 us, with
-// a cluster's join 10 - 13.  4 prompts of 6150 - 8192 tokens, 128 rows x 8 kv heads x 4: 91 us, 680 TFLOP/s.
+// a cluster's join 10 - 14.  4 prompts of 6150 - 8192 tokens, 128 rows x 8 kv heads x 4: 92.5 us, 672 TFLOP/s (91.1 before
+// the sums were made to hold for scales of any distance).
 // Tried and slower: one issuer for both streams, which keeps them in step, so that both want the special-function
 // units at once (0.95 us a unit); codes by cp.async of the converters (0.95 us); four threads per row, whose
 // exchange of maxima costs what it saves (0.97 us); 128-key score tiles (0.97 us); q in shared memory, read again

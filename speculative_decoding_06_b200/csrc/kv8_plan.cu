@@ -14,8 +14,8 @@
 // numbered by the same CTA; for many a second launch spreads them over the GPU,
 // each CTA taking the sums of pages anew from what the first one wrote.  It is
 // bound by latency: a chain of four dependent loads (ids, lengths, ring or
-// table, and the arguments), a scan and the launch: 3.8 us for a step of 4
-// sequences, 8.1 us for 256, 9.6 us for prompts of 128 with the second launch (6.4, 10.3
+// table, and the arguments), a scan and the launch: 3.6 us for a step of 4
+// sequences, 7.9 us for 256, 9.4 us for prompts of 128 with the second launch (6.4, 10.3
 // and 11.5 with a scan of one level and without ids and sums in shared memory).
 #include "common.cuh"
 #include "kv8.h"

@@ -7,8 +7,9 @@ current stream, and no call synchronises or copies to the host.
     pages = cache.page_state(n_seqs, max_blocks)                  # lengths, tables, ring, state: all pages free
     plan = cache.plan(pages.lengths, add, pages.tables, pages.ring, pages.state, max_rows)
     cache.append(layer, k, v, plan.slots)                         # each layer
+    ws = cache.attention_workspace(batch, n_q_heads, max_nodes, max_prefix)       # once, for the largest bounds
     out, lse = cache.attention(layer, q, pages.tables, pages.lengths, offsets, max_prefix=..., k_new=k, v_new=v,
-                               parents=parents)                   # before the rows are appended, or without k_new
+                               parents=parents, workspace=ws)     # before the rows are appended, or without k_new
 """
 
 from __future__ import annotations
@@ -153,7 +154,9 @@ class KV8Cache:
         v_new ([rows][n_kv_heads][128]), the step's own rows (spec_kv8_attention).  Entry b holds rows offsets[b] ..
         offsets[b + 1] - 1, at most max_nodes, of a sequence of at most max_prefix cached tokens.  Returns (out, lse).
         Rows outside every entry, and those of an entry that is out of range (its sequence id, length or row count),
-        are left as they were in `out` and `lse`; where these are new, the former are 0 and -inf, the latter NaN."""
+        are left as they were in `out` and `lse`; where these are new, the former are 0 and -inf, the latter NaN.
+        Without `workspace` each call makes one and clears its first 64 KB.  max_prefix decides how decoding is split: a
+        bound near the longest sequence is faster than the tables' capacity."""
         rc, out, lse = _kv8.attention(*self._id, layer, q, tables, lengths, offsets, max_prefix, max_nodes, k_new,
                                       v_new, parents, seq_ids, scale, out, lse, workspace)
         if rc:
