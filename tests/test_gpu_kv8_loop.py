@@ -226,3 +226,37 @@ def test_export_from_the_engine():
         eng.export_kv8([0], cache, pages, kv8_ids=[1])  # 140 tokens do not fit eight blocks of 16
     assert pages.lengths.tolist() == [0, 70, 0, 33]
     eng.close()
+
+
+@pytest.mark.parametrize("nodes", [(1, 2), (1, 30), (20, 30)])
+def test_two_streams_at_once(nodes):
+    """Calls of two streams over one cache, each with a workspace and outputs of its own (and one with new outputs whose
+    last rows belong to no entry): the same bits as one after the other."""
+    from speculative_decoding_06_b200.kv8 import KV8Cache
+    g = torch.Generator(device="cuda").manual_seed(4)
+    B, P = 3, 3000
+    cache = KV8Cache(1, HKV, 3 * 47, 64)
+    cache.codes.random_(0, 120, generator=g)
+    cache.exps.random_(110, 124, generator=g)
+    lengths, tables = i32([P, 70, 1500]), torch.arange(3 * 47, dtype=torch.int32, device="cuda").view(3, 47)
+    calls = []
+    for n in nodes:
+        q, k, v = (torch.randn(B * n + 2, h, 128, device="cuda", generator=g).half() for h in (HQ, HKV, HKV))
+        ws = cache.attention_workspace(B, HQ, n, P)
+        off = i32(np.arange(B + 1) * n)
+        calls.append(lambda q=q, k=k, v=v, n=n, ws=ws, off=off: cache.attention(
+            0, q, tables, lengths, off, max_prefix=P, max_nodes=n, k_new=k, v_new=v, workspace=ws))
+    want = [c() for c in calls]
+    for (out, lse), n in zip(want, nodes):
+        assert not out[B * n:].any() and (lse[B * n:] == -np.inf).all() and not torch.isnan(out).any()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(40):
+        for c, s in zip(calls, streams):
+            with torch.cuda.stream(s):
+                got.append(c())
+    torch.cuda.synchronize()
+    for i, (out, lse) in enumerate(got):
+        assert torch.equal(out, want[i % 2][0]) and torch.equal(lse, want[i % 2][1])
